@@ -22,6 +22,9 @@
  *      renormalised router probabilities (section «Роутер и top-k gating»).
  * moe_backward differentiates these steps (the choice of experts and the slots pass no
  * gradient); moe_redirect_overflow replaces step 3's dropping by redirection.
+ * The rest of a training step: moe_balance_loss (the auxiliary loss with its gradient),
+ * moe_router_backward (that gradient through the linear router), moe_grad_norm and
+ * moe_adamw_step (the update).
  *
  * Conventions for every call:
  *   - Every pointer is a DEVICE pointer, allocated and owned by the caller, 16-byte aligned.
@@ -325,6 +328,123 @@ moe_status moe_backward(const moe_dims* dims, const uint16_t* x, const float* w_
                         size_t fwd_ws_bytes, const uint16_t* d_out, float* d_x, float* d_w_router,
                         float* d_logit_bias, float* d_w_gate_up, float* d_w_down, void* ws,
                         size_t ws_bytes, void* stream);
+
+/* Balance loss, router z-loss and per-expert counts, with the gradient of the logits.
+ * The first term is the auxiliary loss of moe_router_stats (page «Sparse Mixture-of-Experts»,
+ * section «Маршрутизация токена и auxiliary loss»), over the n tokens that count; the second,
+ * which the pages do not have, keeps the router's logits small:
+ *   p_t = softmax(L_t),  lse_t = log sum_e exp(L_te),  P_e = sum_t p_te / n,
+ *   c_e = counted pairs (t, j) with topk_idx[t, j] = e
+ *   balance = alpha N sum_e (c_e / n) P_e,   z = z_coef sum_t lse_t^2 / n,  loss = balance + z
+ *   d_logits[t, e] = d_loss p_te (alpha N / n (c_e / n - sum_i (c_i / n) p_ti) + 2 z_coef lse_t / n)
+ * (the counts pass no gradient).
+ *   logits      [T, N] fp32, topk_idx [T, k] int32   from moe_route (ids outside [0, N) are not
+ *                                        counted). A logit of -inf has probability 0; a row of
+ *                                        nothing else adds 0 to every sum and has a zero gradient
+ *   token_mask  [T] uint8 or NULL        0: padding. Its logits are not read, whatever they hold;
+ *                                        it counts nowhere and its d_logits row is zero
+ *   d_loss      [1] fp32 or NULL (1)     gradient of the total loss, e.g. a loss scale
+ *   counts      [N] int32 (out)          c_e
+ *   n_tokens    [1] int32 (out)          n. With n = 0 every other output is zero
+ *   prob_mean   [N] fp32 (out)           P_e
+ *   loss        [3] fp32 (out)           balance + z, balance, z
+ *   d_logits    [T, N] fp32 (out) or NULL; must not overlap logits
+ * Deterministic. Uses the per-stage workspace (moe_workspace_bytes). T == 0 launches nothing and
+ * writes nothing, as everywhere. */
+moe_status moe_balance_loss(const moe_dims* dims, const float* logits, const int32_t* topk_idx,
+                            const uint8_t* token_mask, float alpha, float z_coef,
+                            const float* d_loss, int32_t* counts, int32_t* n_tokens,
+                            float* prob_mean, float* loss, float* d_logits, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* Backward pass of the linear router for a dense gradient of the logits, such as
+ * moe_balance_loss writes (moe_backward's own is zero except on the chosen experts):
+ *   d_w_router = d_logits^T x,  d_logit_bias = sum_t d_logits[t],  d_x = d_logits w_router
+ *   x [T, d_model] bf16, w_router [N, d_model] fp32, d_logits [T, N] fp32
+ *   d_x [T, d_model], d_w_router [N, d_model], d_logit_bias [N] fp32 (out), each may be NULL
+ *   accumulate   0: the outputs are written; 1: added to, as after moe_backward, whose outputs
+ *                of the same names have the same shapes
+ *   ws, ws_bytes workspace (moe_router_backward_workspace_bytes), no zeroing needed but for its
+ *                status word (first 256 bytes; read with moe_read_device_error)
+ * Only T, d_model and n_experts of dims matter. Precision: fp32 products and sums (large batches:
+ * on tensor cores, every fp32 operand as three bf16 terms). Deterministic for a given device. */
+moe_status moe_router_backward_workspace_bytes(const moe_dims* dims, size_t* bytes);
+moe_status moe_router_backward(const moe_dims* dims, const uint16_t* x, const float* w_router,
+                               const float* d_logits, float* d_x, float* d_w_router,
+                               float* d_logit_bias, int32_t accumulate, void* ws, size_t ws_bytes,
+                               void* stream);
+
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1 } moe_dtype;
+
+/* One gradient of moe_grad_norm: numel elements of dtype at grad (may be NULL if numel is 0). */
+typedef struct {
+  const void* grad;
+  int64_t numel;
+  int32_t dtype; /* moe_dtype */
+} moe_grad_tensor;
+
+/* Global norm of n gradients and the scale that clips it:
+ *   norm  [1] fp32 (out)   sqrt(sum of the squares of all elements)
+ *   scale [1] fp32 (out)   min(1, max_norm / (norm + 1e-6)); NaN if norm is not finite (a NaN or
+ *                          an infinity among the gradients, or squares past fp32's range), which
+ *                          makes moe_adamw_step leave the step out. max_norm > 0, may be infinite
+ * `tensors` is a host array, read during the call. n may be 0. Deterministic.
+ * ws: moe_grad_norm_workspace_bytes, zeroed once before its first use. */
+moe_status moe_grad_norm_workspace_bytes(size_t* bytes);
+moe_status moe_grad_norm(const moe_grad_tensor* tensors, int32_t n, float max_norm, float* norm,
+                         float* scale, void* ws, size_t ws_bytes, void* stream);
+
+/* Elements that share a scale where the moments are held in 8 bits. */
+#define MOE_ADAMW_BLOCK 128
+
+/* One tensor of moe_adamw_step; numel elements, contiguous. Nothing may overlap.
+ *   param        fp32 or bf16 (param_dtype); updated
+ *   master       fp32 master copy of a bf16 param, updated, of which param becomes the nearest
+ *                bf16; NULL: none. A bf16 param without one is updated in fp32 and rounded up
+ *                or down with the probability of what is cut off (see seed)
+ *   grad         fp32 or bf16 (grad_dtype)
+ *   m, v         the moments; state_bits 32: fp32. state_bits 8: E4M3 codes of m and of sqrt(v)
+ *                (bytes), with one fp32 scale per MOE_ADAMW_BLOCK elements, m = code m_scale and
+ *                v = (code v_scale)^2. A block's new scale is its largest magnitude / 448; a
+ *                value is rounded up with the probability of what is cut off; a nonzero v keeps a
+ *                nonzero code; a block whose largest magnitude is below 2^-96 becomes zeros. This
+ *                step's update uses the moments before that rounding. All zeros to begin with
+ *   m_scale, v_scale  [ceil(numel / MOE_ADAMW_BLOCK)] fp32, state_bits 8 only */
+typedef struct {
+  void* param;
+  float* master;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t numel;
+  int32_t param_dtype;
+  int32_t grad_dtype;
+  int32_t state_bits;
+  float weight_decay;
+} moe_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps; /* 0 <= beta < 1, eps > 0 */
+  int32_t step;                 /* t of the bias corrections, 1 in the first step */
+  uint32_t seed;                /* of the stochastic roundings */
+  const int32_t* step_dev;      /* device int32 or NULL: t, in place of step, read when the kernel
+                                   runs (for captured graphs); below 1 the step is left out */
+  const float* lr_dev;          /* device fp32 or NULL: in place of lr */
+  const float* grad_scale;      /* device fp32 or NULL (1): multiplies every gradient. Not finite:
+                                   the step is left out, nothing is written */
+} moe_adamw_config;
+
+/* One AdamW step (decoupled weight decay) over n tensors at once:
+ *   g' = g grad_scale,  m' = beta1 m + (1 - beta1) g',  v' = beta2 v + (1 - beta2) g'^2,
+ *   p' = p (1 - lr wd) - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
+ * in fp32. The random bits of a rounding depend on seed, t, the tensor's place in the list and
+ * the element, so equal calls give equal results. `tensors` and `config` are host memory, read
+ * during the call; a graph that captures the call keeps the pointers that they held. Up to 384
+ * tensors take one launch. No workspace. */
+moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n,
+                          const moe_adamw_config* config, void* stream);
 
 /* Expert weights in an MX format (device pointers, 16-byte aligned):
  *   fmt             MOE_WFMT_MXFP8 or MOE_WFMT_MXFP4

@@ -15,3 +15,5 @@ from .mx_oracle import (MX_BLOCK, decode_e8m0, decode_e4m3, decode_e2m1,  # noqa
 from .moe_backward import (logistic, silu_derivative, gelu_derivative,  # noqa: F401
                            combine_backward, renormalise_backward, expert_backward, aux_loss_backward,
                            moe_layer_backward)
+from .moe_training import (balance_loss, router_backward, grad_norm, random_bits,  # noqa: F401
+                           round_up_by_chance, quantise_moment, adamw, ADAMW_BLOCK)

@@ -65,6 +65,29 @@ class MxWeights(ctypes.Structure):
                 ("down_scales", ctypes.c_void_p)]
 
 
+ADAMW_BLOCK = 128  # MOE_ADAMW_BLOCK: elements that share a scale of 8-bit moments
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}  # moe_dtype
+
+
+class GradTensor(ctypes.Structure):
+    """``moe_grad_tensor``: one gradient of moe_grad_norm."""
+    _fields_ = [("grad", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class AdamWTensor(ctypes.Structure):
+    """``moe_adamw_tensor``: one tensor of moe_adamw_step."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("numel", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32), ("weight_decay", ctypes.c_float)]
+
+
+class AdamWConfig(ctypes.Structure):
+    """``moe_adamw_config``: hyper-parameters of a step."""
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + [
+        ("step", ctypes.c_int32), ("seed", ctypes.c_uint32), ("step_dev", ctypes.c_void_p),
+        ("lr_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _DIMS = ctypes.POINTER(Dims)
 _MXW = ctypes.POINTER(MxWeights)
@@ -94,6 +117,16 @@ _SIGS = {
     "moe_backward_workspace_bytes": (ctypes.c_int, [_DIMS, ctypes.POINTER(ctypes.c_size_t)]),
     "moe_backward": (ctypes.c_int, [_DIMS, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P, _P, _P,
                                     _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_balance_loss": (ctypes.c_int, [_DIMS, _P, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _P,
+                                        _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_router_backward_workspace_bytes": (ctypes.c_int, [_DIMS, ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_router_backward": (ctypes.c_int, [_DIMS, _P, _P, _P, _P, _P, _P, ctypes.c_int32, _P,
+                                           ctypes.c_size_t, _P]),
+    "moe_grad_norm_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_grad_norm": (ctypes.c_int, [ctypes.POINTER(GradTensor), ctypes.c_int32, ctypes.c_float, _P, _P,
+                                     _P, ctypes.c_size_t, _P]),
+    "moe_adamw_step": (ctypes.c_int, [ctypes.POINTER(AdamWTensor), ctypes.c_int32,
+                                      ctypes.POINTER(AdamWConfig), _P]),
     "moe_read_device_error": (ctypes.c_int, [_P, _P, ctypes.POINTER(ctypes.c_int)]),
     "moe_debug_set_wait_timeout_ns": (ctypes.c_uint64, [ctypes.c_uint64]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -452,3 +485,179 @@ def backward_into(dims: Dims, x, w_router, w_gate_up, w_down, fwd_ws, d_out, d_x
         _ptr(d_w_gate_up, "d_w_gate_up", torch.float32, (N, rows, d)),
         _ptr(d_w_down, "d_w_down", torch.float32, (N, d, F)),
         _ptr(ws, "ws", torch.uint8), _nbytes(ws), _stream(stream)), "moe_backward")
+
+
+# ----------------------------------------------------------------------------- training
+def _one_device(**tensors) -> None:
+    """All tensors on the current device: the library launches there."""
+    here = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda and t.device.index != here:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+
+
+def balance_loss(dims: Dims, logits, topk_idx, token_mask, counts, n_tokens, prob_mean, loss,
+                 d_logits, ws, alpha: float = 1e-2, z_coef: float = 0.0, d_loss=None,
+                 stream=None) -> None:
+    """Balance loss and router z-loss over the tokens whose token_mask (uint8 or None) is not 0,
+    per-expert counts, and the gradient of the logits (d_logits may be None). loss [3] receives
+    balance + z, balance, z; d_loss, a scalar tensor or None (1), is the total's gradient."""
+    T, N, k = dims.T, dims.n_experts, dims.top_k
+    _one_device(logits=logits, topk_idx=topk_idx, token_mask=token_mask, counts=counts,
+                n_tokens=n_tokens, prob_mean=prob_mean, loss=loss, d_logits=d_logits, ws=ws,
+                d_loss=d_loss)
+    _check(_lib.moe_balance_loss(
+        ctypes.byref(dims), _ptr(logits, "logits", torch.float32, (T, N)),
+        _ptr(topk_idx, "topk_idx", torch.int32, (T, k)),
+        _ptr(token_mask, "token_mask", torch.uint8, (T,), allow_none=True), float(alpha), float(z_coef),
+        _ptr(d_loss, "d_loss", torch.float32, None if d_loss is None or d_loss.dim() == 0 else (1,),
+             allow_none=True),
+        _ptr(counts, "counts", torch.int32, (N,)), _ptr(n_tokens, "n_tokens", torch.int32, (1,)),
+        _ptr(prob_mean, "prob_mean", torch.float32, (N,)), _ptr(loss, "loss", torch.float32, (3,)),
+        _ptr(d_logits, "d_logits", torch.float32, (T, N), allow_none=True),
+        _ptr(ws, "ws", torch.uint8), _nbytes(ws), _stream(stream)), "moe_balance_loss")
+
+
+def router_backward_workspace_bytes(dims: Dims) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.moe_router_backward_workspace_bytes(ctypes.byref(dims), ctypes.byref(n)),
+           "moe_router_backward_workspace_bytes")
+    return int(n.value)
+
+
+def new_router_backward_workspace(dims: Dims, device=None) -> torch.Tensor:
+    return torch.zeros(router_backward_workspace_bytes(dims), dtype=torch.uint8, device=device or "cuda")
+
+
+def router_backward(dims: Dims, x, w_router, d_logits, d_x, d_w_router, d_logit_bias, ws,
+                    accumulate: bool = False, stream=None) -> None:
+    """Gradient of the linear router for a dense gradient of the logits; outputs (each may be
+    None) are written, or added to with accumulate (after backward_into)."""
+    T, d, N = dims.T, dims.d_model, dims.n_experts
+    _one_device(x=x, w_router=w_router, d_logits=d_logits, d_x=d_x, d_w_router=d_w_router,
+                d_logit_bias=d_logit_bias, ws=ws)
+    _check(_lib.moe_router_backward(
+        ctypes.byref(dims), _ptr(x, "x", torch.bfloat16, (T, d)),
+        _ptr(w_router, "w_router", torch.float32, (N, d)),
+        _ptr(d_logits, "d_logits", torch.float32, (T, N)),
+        _ptr(d_x, "d_x", torch.float32, (T, d), allow_none=True),
+        _ptr(d_w_router, "d_w_router", torch.float32, (N, d), allow_none=True),
+        _ptr(d_logit_bias, "d_logit_bias", torch.float32, (N,), allow_none=True),
+        1 if accumulate else 0, _ptr(ws, "ws", torch.uint8), _nbytes(ws), _stream(stream)),
+        "moe_router_backward")
+
+
+class _Plan:
+    """A host array of tensor descriptors, with the tensors it points at."""
+
+    def __init__(self, kind, items, refs):
+        self.array = (kind * max(1, len(items)))(*items)
+        self.n = len(items)
+        self.refs = refs
+        devices = {t.device for r in refs for t in r if t is not None}
+        if len(devices) > 1:
+            raise ValueError(f"the tensors are on several devices: {sorted(map(str, devices))}")
+        self.device = next(iter(devices), None)
+
+    def check_device(self) -> None:
+        if self.device is not None and self.device.index != torch.cuda.current_device():
+            raise ValueError(f"the tensors are on {self.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+
+
+def grad_plan(grads) -> _Plan:
+    """Descriptors of gradients (fp32 or bf16 tensors of any shape) for grad_norm."""
+    grads = list(grads)
+    items = []
+    for i, g in enumerate(grads):
+        if g.dtype not in _DTYPES:
+            raise ValueError(f"gradient {i} must be fp32 or bf16, got {g.dtype}")
+        items.append(GradTensor(_ptr(g, f"gradient {i}"), g.numel(), _DTYPES[g.dtype]))
+    return _Plan(GradTensor, items, [(g,) for g in grads])
+
+
+def new_grad_norm_workspace(device=None) -> torch.Tensor:
+    n = ctypes.c_size_t(0)
+    _check(_lib.moe_grad_norm_workspace_bytes(ctypes.byref(n)), "moe_grad_norm_workspace_bytes")
+    return torch.zeros(int(n.value), dtype=torch.uint8, device=device or "cuda")
+
+
+def grad_norm(plan: _Plan, max_norm: float, norm, scale, ws, stream=None) -> None:
+    """norm [1]: the global norm of the plan's gradients; scale [1]: min(1, max_norm / (norm +
+    1e-6)), or NaN (adamw_step then leaves the step out) where the norm is not finite."""
+    plan.check_device()
+    _one_device(norm=norm, scale=scale, ws=ws)
+    if plan.array._type_ is not GradTensor:
+        raise ValueError("grad_norm takes a plan of grad_plan()")
+    _check(_lib.moe_grad_norm(plan.array, plan.n, float(max_norm), _ptr(norm, "norm", torch.float32, (1,)),
+                              _ptr(scale, "scale", torch.float32, (1,)), _ptr(ws, "ws", torch.uint8),
+                              _nbytes(ws), _stream(stream)), "moe_grad_norm")
+
+
+def new_adamw_state(param: torch.Tensor, bits: int = 32) -> dict:
+    """Zeroed moments of a parameter: m and v (fp32, or E4M3 codes with m_scale and v_scale)."""
+    n = param.numel()
+    if bits == 32:
+        return {"m": torch.zeros(n, dtype=torch.float32, device=param.device),
+                "v": torch.zeros(n, dtype=torch.float32, device=param.device)}
+    if bits != 8:
+        raise ValueError("bits must be 32 or 8")
+    blocks = -(-n // ADAMW_BLOCK)
+    codes = lambda: torch.zeros(n, dtype=torch.uint8, device=param.device).view(torch.float8_e4m3fn)
+    return {"m": codes(), "v": codes(),
+            "m_scale": torch.zeros(blocks, dtype=torch.float32, device=param.device),
+            "v_scale": torch.zeros(blocks, dtype=torch.float32, device=param.device)}
+
+
+def adamw_tensor(param, grad, m, v, *, master=None, m_scale=None, v_scale=None,
+                 weight_decay: float = 0.0) -> tuple:
+    """One tensor of an AdamW plan: param fp32 or bf16, grad fp32 or bf16, m and v both fp32 or
+    both float8_e4m3fn (codes of m and of sqrt(v), with m_scale and v_scale [ceil(numel / 128)]).
+    master: fp32 master copy of a bf16 param. The shapes may differ as long as numel agrees."""
+    n = param.numel()
+    for name, t in (("param", param), ("grad", grad)):
+        if t.dtype not in _DTYPES:
+            raise ValueError(f"{name} must be fp32 or bf16, got {t.dtype}")
+    if m.dtype != v.dtype or m.dtype not in (torch.float32, torch.float8_e4m3fn):
+        raise ValueError(f"m and v must both be fp32 or both float8_e4m3fn, got {m.dtype} and {v.dtype}")
+    if master is not None and param.dtype != torch.bfloat16:
+        raise ValueError("master goes with a bf16 param")
+    eight = m.dtype == torch.float8_e4m3fn
+    if eight != (m_scale is not None) or eight != (v_scale is not None):
+        raise ValueError("m_scale and v_scale go with 8-bit moments, and only with them")
+    for name, t in (("grad", grad), ("m", m), ("v", v), ("master", master)):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+    blocks = (-(-n // ADAMW_BLOCK),)
+    d = AdamWTensor(_ptr(param, "param"), _ptr(master, "master", torch.float32, allow_none=True),
+                    _ptr(grad, "grad"), _ptr(m, "m"), _ptr(v, "v"),
+                    _ptr(m_scale, "m_scale", torch.float32, blocks, allow_none=True),
+                    _ptr(v_scale, "v_scale", torch.float32, blocks, allow_none=True), n,
+                    _DTYPES[param.dtype], _DTYPES[grad.dtype], 8 if eight else 32, float(weight_decay))
+    return d, (param, grad, m, v, master, m_scale, v_scale)
+
+
+def adamw_plan(tensors) -> _Plan:
+    """Descriptors of many tensors (from adamw_tensor) for adamw_step, made once and used for
+    every step: the plan keeps the tensors alive and their addresses."""
+    tensors = list(tensors)
+    return _Plan(AdamWTensor, [d for d, _ in tensors], [r for _, r in tensors])
+
+
+def adamw_step(plan: _Plan, step, *, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, seed: int = 0,
+               grad_scale=None, stream=None) -> None:
+    """One AdamW step over the plan's tensors. step: the number of this step, from 1, or an int32
+    tensor [1] read when the kernel runs; lr: a number or an fp32 tensor [1] read likewise;
+    grad_scale: fp32 tensor [1] (from grad_norm) or None."""
+    plan.check_device()
+    if plan.array._type_ is not AdamWTensor:
+        raise ValueError("adamw_step takes a plan of adamw_plan()")
+    step_t = step if isinstance(step, torch.Tensor) else None
+    lr_t = lr if isinstance(lr, torch.Tensor) else None
+    _one_device(step=step_t, lr=lr_t, grad_scale=grad_scale)
+    cfg = AdamWConfig(0.0 if lr_t is not None else float(lr), float(betas[0]), float(betas[1]), float(eps),
+                      1 if step_t is not None else int(step), int(seed) & 0xFFFFFFFF,
+                      _ptr(step_t, "step", torch.int32, (1,), allow_none=True),
+                      _ptr(lr_t, "lr", torch.float32, (1,), allow_none=True),
+                      _ptr(grad_scale, "grad_scale", torch.float32, (1,), allow_none=True))
+    _check(_lib.moe_adamw_step(plan.array, plan.n, ctypes.byref(cfg), _stream(stream)), "moe_adamw_step")

@@ -126,7 +126,8 @@ size_t shared_region_bytes(const moe_dims* d) {
   const size_t ffn = round_up(ffn_plan(d).part_bytes, 256);
   const size_t stats = round_up(moe::router_stats_scratch_bytes(d->T, d->n_experts), 256);
   const size_t redirect = round_up(moe::redirect_scratch_bytes(d->T, d->top_k), 256);
-  return std::max(std::max(std::max(routing, ffn), stats), redirect);
+  const size_t balance = round_up(moe::balance_scratch_bytes(d->T, d->n_experts, d->top_k), 256);
+  return std::max({routing, ffn, stats, redirect, balance});
 }
 
 size_t stage_ws_bytes(const moe_dims* d) {
@@ -646,6 +647,142 @@ moe_status moe_backward(const moe_dims* dims, const uint16_t* x, const float* w_
   a.r_max = max_rows(dims);
   a.timeout_ns = moe::wait_timeout_ns();
   return launch_status(moe::launch_backward(a, as_stream(stream)));
+}
+
+moe_status moe_balance_loss(const moe_dims* dims, const float* logits, const int32_t* topk_idx,
+                            const uint8_t* token_mask, float alpha, float z_coef,
+                            const float* d_loss, int32_t* counts, int32_t* n_tokens,
+                            float* prob_mean, float* loss, float* d_logits, void* ws,
+                            size_t ws_bytes, void* stream) {
+  moe_status st = check_dims(dims);
+  if (st != MOE_OK) return st;
+  if (dims->T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !counts || !n_tokens || !prob_mean || !loss || !ws)
+    return MOE_ERR_INVALID;
+  if (!isfinite(alpha) || !isfinite(z_coef)) return MOE_ERR_INVALID;
+  if (!aligned16(logits) || !aligned16(topk_idx) || (token_mask && !aligned16(token_mask)) ||
+      !aligned16(counts) || !aligned16(prob_mean) || !aligned16(loss) ||
+      (d_logits && !aligned16(d_logits)) || !aligned16(ws))
+    return MOE_ERR_UNSUPPORTED;
+  if (ws_bytes < stage_ws_bytes(dims)) return MOE_ERR_WORKSPACE;
+  if ((st = check_device()) != MOE_OK) return st;
+  moe::BalanceArgs a{};
+  a.logits = logits;
+  a.topk_idx = topk_idx;
+  a.token_mask = token_mask;
+  a.d_loss = d_loss;
+  a.alpha = alpha;
+  a.z_coef = z_coef;
+  a.counts = counts;
+  a.n_tokens = n_tokens;
+  a.prob_mean = prob_mean;
+  a.loss = loss;
+  a.d_logits = d_logits;
+  a.scratch = shared_region_of(dims, ws);
+  a.counter = reinterpret_cast<int*>(static_cast<char*>(ws) + moe::kBalanceCounterOffset);
+  a.T = dims->T;
+  a.N = dims->n_experts;
+  a.k = dims->top_k;
+  return launch_status(moe::launch_balance_loss(a, as_stream(stream)));
+}
+
+moe_status moe_router_backward_workspace_bytes(const moe_dims* dims, size_t* bytes) {
+  const moe_status st = check_dims(dims);
+  if (st != MOE_OK) return st;
+  if (bytes == nullptr) return MOE_ERR_INVALID;
+  *bytes = moe::kStatusBytes +
+           round_up(moe::router_backward_scratch_bytes(dims->T, dims->n_experts, dims->d_model), 256);
+  return MOE_OK;
+}
+
+moe_status moe_router_backward(const moe_dims* dims, const uint16_t* x, const float* w_router,
+                               const float* d_logits, float* d_x, float* d_w_router,
+                               float* d_logit_bias, int32_t accumulate, void* ws, size_t ws_bytes,
+                               void* stream) {
+  moe_status st = check_dims(dims);
+  if (st != MOE_OK) return st;
+  if (dims->T == 0) return MOE_OK;
+  if (!x || !w_router || !d_logits || !ws) return MOE_ERR_INVALID;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID;
+  if (!aligned16(x) || !aligned16(w_router) || !aligned16(d_logits) || (d_x && !aligned16(d_x)) ||
+      (d_w_router && !aligned16(d_w_router)) || (d_logit_bias && !aligned16(d_logit_bias)) ||
+      !aligned16(ws))
+    return MOE_ERR_UNSUPPORTED;
+  size_t need = 0;
+  moe_router_backward_workspace_bytes(dims, &need);
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if ((st = check_device()) != MOE_OK) return st;
+  moe::RouterBackwardArgs a{};
+  a.x = x;
+  a.w_router = w_router;
+  a.d_logits = d_logits;
+  a.d_x = d_x;
+  a.d_w_router = d_w_router;
+  a.d_logit_bias = d_logit_bias;
+  a.accumulate = accumulate;
+  a.scratch = static_cast<char*>(ws) + moe::kStatusBytes;
+  a.T = dims->T;
+  a.N = dims->n_experts;
+  a.d = dims->d_model;
+  a.status = status_of(ws);
+  a.timeout_ns = moe::wait_timeout_ns();
+  return launch_status(moe::launch_router_backward(a, as_stream(stream)));
+}
+
+moe_status moe_grad_norm_workspace_bytes(size_t* bytes) {
+  if (bytes == nullptr) return MOE_ERR_INVALID;
+  *bytes = moe::kStatusBytes + moe::kGradNormSlots * sizeof(double);
+  return MOE_OK;
+}
+
+moe_status moe_grad_norm(const moe_grad_tensor* tensors, int32_t n, float max_norm, float* norm,
+                         float* scale, void* ws, size_t ws_bytes, void* stream) {
+  if (n < 0 || (n > 0 && tensors == nullptr) || !norm || !scale || !ws) return MOE_ERR_INVALID;
+  if (!(max_norm > 0.f)) return MOE_ERR_INVALID;
+  for (int32_t i = 0; i < n; ++i) {
+    const moe_grad_tensor& t = tensors[i];
+    if (t.numel < 0 || (t.numel > 0 && t.grad == nullptr)) return MOE_ERR_INVALID;
+    if (t.dtype != MOE_DTYPE_F32 && t.dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID;
+    if (!aligned16(t.grad)) return MOE_ERR_UNSUPPORTED;
+  }
+  if (!aligned16(ws)) return MOE_ERR_UNSUPPORTED;
+  size_t need = 0;
+  moe_grad_norm_workspace_bytes(&need);
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  const moe_status st = check_device();
+  if (st != MOE_OK) return st;
+  return launch_status(moe::launch_grad_norm(tensors, n, max_norm, norm, scale, ws, as_stream(stream)));
+}
+
+moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n,
+                          const moe_adamw_config* config, void* stream) {
+  if (n < 0 || (n > 0 && tensors == nullptr) || config == nullptr) return MOE_ERR_INVALID;
+  const moe_adamw_config& c = *config;
+  if (!isfinite(c.lr) || !(c.beta1 >= 0.0 && c.beta1 < 1.0) || !(c.beta2 >= 0.0 && c.beta2 < 1.0) ||
+      !(c.eps > 0.0) || !isfinite(c.eps))
+    return MOE_ERR_INVALID;
+  if (c.step_dev == nullptr && c.step < 1) return MOE_ERR_INVALID;
+  bool any = false;
+  for (int32_t i = 0; i < n; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.numel < 0 || !isfinite(t.weight_decay)) return MOE_ERR_INVALID;
+    if ((t.param_dtype != MOE_DTYPE_F32 && t.param_dtype != MOE_DTYPE_BF16) ||
+        (t.grad_dtype != MOE_DTYPE_F32 && t.grad_dtype != MOE_DTYPE_BF16) ||
+        (t.state_bits != 32 && t.state_bits != 8))
+      return MOE_ERR_INVALID;
+    if (t.master != nullptr && t.param_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID;
+    if (t.numel == 0) continue;
+    any = true;
+    if (!t.param || !t.grad || !t.m || !t.v) return MOE_ERR_INVALID;
+    if (t.state_bits == 8 && (!t.m_scale || !t.v_scale)) return MOE_ERR_INVALID;
+    if (!aligned16(t.param) || !aligned16(t.master) || !aligned16(t.grad) || !aligned16(t.m) ||
+        !aligned16(t.v) || !aligned16(t.m_scale) || !aligned16(t.v_scale))
+      return MOE_ERR_UNSUPPORTED;
+  }
+  if (!any) return MOE_OK;
+  const moe_status st = check_device();
+  if (st != MOE_OK) return st;
+  return launch_status(moe::launch_adamw(tensors, n, c, as_stream(stream)));
 }
 
 namespace {

@@ -1,0 +1,379 @@
+// Load-balancing loss and router z-loss with their gradient, per-expert counts, padding mask.
+//
+// With p_t = softmax(L_t), n the number of tokens that count, c_e the (token, choice) pairs of
+// those tokens that chose expert e, and P_e = sum_t p_te / n (page «Sparse Mixture-of-Experts»,
+// section «Маршрутизация токена и auxiliary loss», for the first term):
+//   loss = alpha N sum_e (c_e / n) P_e + z sum_t lse_t^2 / n,   lse_t = log sum_e exp(L_te)
+//   dL_te = g p_te [alpha N / n (c_e / n - sum_i (c_i / n) p_ti) + 2 z lse_t / n]
+// g being the upstream gradient; the counts pass none. The gradient needs the counts of the
+// whole batch but not P, so one pass over the logits gives everything: the counts come first,
+// from topk_idx alone (4 k bytes a token against 4 N), and every CTA holds them while it reads
+// its tokens' logits once and writes their gradients.
+//
+//   pass 1 (only past kInlinePairs pairs)  per-chunk counts, one row of the workspace a chunk
+//   pass 2  the counts (of the rows, or of topk_idx itself), then the tokens; P's partial sums
+//           leave one row a CTA, and the last CTA to finish adds the rows in order
+// No floating-point atomics: the results do not depend on the order the CTAs run in.
+// Bound by memory: 8 T N bytes with the gradient, about 10 instructions a logit.
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kBalThreads = 512;
+constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kMaxN = 256;
+// Up to here every CTA counts all pairs itself; past it the pairs are counted in chunks first.
+constexpr int64_t kInlinePairs = 4096;
+constexpr int kCountRows = 64;  // rows of partial counts, at most
+
+struct CountPlan {
+  int64_t chunk;  // tokens a row
+  int rows;       // 0: counted inline
+};
+CountPlan count_plan(int64_t T, int64_t k) {
+  if (T * k <= kInlinePairs) return {0, 0};
+  const int64_t want = std::min<int64_t>(kCountRows, (T * k + kInlinePairs - 1) / kInlinePairs);
+  const int64_t chunk = (T + want - 1) / want;
+  return {chunk, static_cast<int>((T + chunk - 1) / chunk)};
+}
+
+// Lanes a token takes (G), loads a lane makes of its row (C) and values a load brings (VEC = 4
+// where rows are 16-byte aligned): G * C * VEC >= N, G as small as that allows with C = 1.
+struct TokenShape {
+  int g, c, vec;
+};
+TokenShape token_shape(int N) {
+  if (N % 4 == 0)
+    return N <= 16 ? TokenShape{4, 1, 4} : N <= 32 ? TokenShape{8, 1, 4}
+         : N <= 64 ? TokenShape{16, 1, 4} : N <= 128 ? TokenShape{32, 1, 4} : TokenShape{32, 2, 4};
+  return N <= 8 ? TokenShape{8, 1, 1} : N <= 16 ? TokenShape{16, 1, 1} : N <= 32 ? TokenShape{32, 1, 1}
+       : N <= 64 ? TokenShape{32, 2, 1} : N <= 128 ? TokenShape{32, 4, 1} : TokenShape{32, 8, 1};
+}
+
+// CTAs of pass 2: one an SM, fewer when the tokens do not fill them.
+int balance_ctas(int T, int N, int sms) {
+  const int per_cta = kBalWarps * (32 / token_shape(N).g);
+  return std::max(1, std::min((T + per_cta - 1) / per_cta, sms));
+}
+// floats of a CTA's row: N probabilities rounded up to four, then sum of lse^2 and padding
+__host__ __device__ constexpr int row_floats(int N) { return (N + 3) / 4 * 4 + 4; }
+
+// Counts of tokens [t0, t1): pairs of counted tokens that chose expert e into s_cnt[e], counted
+// tokens into s_cnt[N]. Integer shared-memory atomics: the result has no order.
+__device__ __forceinline__ void count_pairs(const int32_t* __restrict__ topk_idx,
+                                            const uint8_t* __restrict__ mask, int64_t t0, int64_t t1,
+                                            int N, int k, int* s_cnt) {
+  const int64_t q1 = t1 * k;
+  for (int64_t q = t0 * k + threadIdx.x; q < q1; q += kBalThreads) {
+    const int e = topk_idx[q];
+    if (e >= 0 && e < N && (mask == nullptr || mask[q / k] != 0)) atomicAdd(&s_cnt[e], 1);
+  }
+  int n = 0;
+  if (mask == nullptr) {
+    if (threadIdx.x == 0) n = static_cast<int>(t1 - t0);
+  } else {
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += kBalThreads) n += mask[t] != 0;
+  }
+  n = __reduce_add_sync(kFull, n);
+  if ((threadIdx.x & 31) == 0 && n != 0) atomicAdd(&s_cnt[N], n);
+}
+
+__global__ void __launch_bounds__(kBalThreads) balance_count_kernel(
+    const int32_t* __restrict__ topk_idx, const uint8_t* __restrict__ mask,
+    int32_t* __restrict__ rows, int T, int64_t chunk, int N, int k) {
+  __shared__ int s_cnt[kMaxN + 1];
+  pdl_trigger();
+  for (int e = threadIdx.x; e <= N; e += kBalThreads) s_cnt[e] = 0;
+  pdl_wait();
+  __syncthreads();
+  const int64_t t0 = blockIdx.x * chunk;
+  count_pairs(topk_idx, mask, t0, min(static_cast<int64_t>(T), t0 + chunk), N, k, s_cnt);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= N; e += kBalThreads) rows[blockIdx.x * (N + 1) + e] = s_cnt[e];
+}
+
+struct BalanceParams {
+  const float* logits;
+  const int32_t* topk_idx;
+  const uint8_t* mask;
+  const float* d_loss;
+  float alpha, z_coef;
+  int32_t* counts;
+  int32_t* n_tokens;
+  float* prob_mean;
+  float* loss;
+  float* d_logits;
+  const int32_t* count_rows;
+  int n_count_rows;
+  float* part;   // [gridDim.x][row_floats(N)]
+  int* counter;  // zero between calls
+  int T, N, k;
+};
+
+template <int G, int C, int VEC>
+__global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const BalanceParams a) {
+  constexpr int V = C * VEC;          // values a lane holds of a token
+  constexpr int kGroups = 32 / G;     // tokens a warp takes at once
+  __shared__ int s_cnt[kMaxN + 1];
+  __shared__ float s_acc[kBalWarps][G * V];
+  __shared__ float s_z[kBalWarps];
+  __shared__ float4 s_red[kBalThreads];
+  __shared__ int s_last;
+  const int N = a.N;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e <= N; e += kBalThreads) s_cnt[e] = 0;
+  pdl_trigger();
+  pdl_wait();
+  __syncthreads();
+  if (a.n_count_rows == 0) {
+    count_pairs(a.topk_idx, a.mask, 0, a.T, N, a.k, s_cnt);
+  } else {
+    const int items = a.n_count_rows * (N + 1);
+    for (int i = threadIdx.x; i < items; i += kBalThreads) {
+      const int c = __ldcg(a.count_rows + i);
+      if (c != 0) atomicAdd(&s_cnt[i % (N + 1)], c);
+    }
+  }
+  __syncthreads();
+  const int n = s_cnt[N];
+  if (blockIdx.x == 0) {
+    for (int e = threadIdx.x; e < N; e += kBalThreads) a.counts[e] = s_cnt[e];
+    if (threadIdx.x == 0) *a.n_tokens = n;
+  }
+  const float inv_n = 1.0f / static_cast<float>(max(n, 1));
+  const float g = a.d_loss != nullptr ? *a.d_loss : 1.0f;
+  const float c_bal = g * a.alpha * static_cast<float>(N) * inv_n;
+  const float c_z = g * 2.0f * a.z_coef * inv_n;
+  const int gl = lane % G;  // lane within the token's group
+  float f[V], acc[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int e = (j / VEC * G + gl) * VEC + j % VEC;
+    f[j] = e < N ? static_cast<float>(s_cnt[e]) * inv_n : 0.f;
+    acc[j] = 0.f;
+  }
+  float z_acc = 0.f;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kBalWarps * kGroups;
+  for (int64_t t = (blockIdx.x * kBalWarps + warp) * kGroups + lane / G; t - lane / G < a.T; t += stride) {
+    const bool have = t < a.T;
+    const bool counted = have && (a.mask == nullptr || a.mask[t] != 0);
+    const int64_t row = t * N;
+    float v[V];
+    float m = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int e = (c * G + gl) * VEC;
+      if (VEC == 4) {
+        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (counted && e < N) q = __ldg(reinterpret_cast<const float4*>(a.logits + row + e));
+        v[c * VEC] = q.x;
+        v[c * VEC + VEC / 4] = q.y;
+        v[c * VEC + VEC / 2] = q.z;
+        v[c * VEC + VEC * 3 / 4] = q.w;
+      } else {
+        v[c] = counted && e < N ? __ldg(a.logits + row + e) : -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) m = fmaxf(m, v[j]);
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    const float base = m == -INFINITY ? 0.f : m;  // a row of -inf only (or one that is not counted)
+    float sum = 0.f, inner = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      v[j] = expf(v[j] - base);
+      sum += v[j];
+      inner += v[j] * f[j];
+    }
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(kFull, sum, o);
+      inner += __shfl_xor_sync(kFull, inner, o);
+    }
+    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+    const float lse = sum > 0.f ? base + logf(sum) : 0.f;
+    inner *= inv;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      v[j] *= inv;
+      acc[j] += v[j];
+    }
+    if (gl == 0) z_acc += lse * lse;
+    if (a.d_logits != nullptr && have) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] *= c_bal * (f[j] - inner) + c_z * lse;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int e = (c * G + gl) * VEC;
+        if (e < N) {
+          if (VEC == 4)
+            *reinterpret_cast<float4*>(a.d_logits + row + e) =
+                make_float4(v[c * VEC], v[c * VEC + VEC / 4], v[c * VEC + VEC / 2], v[c * VEC + VEC * 3 / 4]);
+          else
+            a.d_logits[row + e] = v[c];
+        }
+      }
+    }
+  }
+  // P's partial sums: groups of a warp, then the warps in order
+#pragma unroll
+  for (int o = G; o < 32; o <<= 1) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] += __shfl_xor_sync(kFull, acc[j], o);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z_acc += __shfl_xor_sync(kFull, z_acc, o);
+  if (lane < G) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) s_acc[warp][(j / VEC * G + gl) * VEC + j % VEC] = acc[j];
+  }
+  if (lane == 0) s_z[warp] = z_acc;
+  __syncthreads();
+  const int rf = row_floats(N);
+  float* my_row = a.part + static_cast<int64_t>(blockIdx.x) * rf;
+  for (int e = threadIdx.x; e < rf; e += kBalThreads) {
+    float s = 0.f;
+    if (e < N)
+      for (int w = 0; w < kBalWarps; ++w) s += s_acc[w][e];
+    else if (e == rf - 4)
+      for (int w = 0; w < kBalWarps; ++w) s += s_z[w];
+    my_row[e] = s;
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = atomicAdd(a.counter, 1) == static_cast<int>(gridDim.x) - 1;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  // rows in order, four columns a thread: the threads of a column take a contiguous range of the
+  // rows each, and their sums are added in range order
+  const int quads = rf / 4;
+  const int ranges = kBalThreads / quads;
+  const int q = threadIdx.x % quads, r = threadIdx.x / quads;
+  float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r < ranges) {
+    const int n_rows = gridDim.x;
+    const int r0 = static_cast<int>(static_cast<int64_t>(n_rows) * r / ranges);
+    const int r1 = static_cast<int>(static_cast<int64_t>(n_rows) * (r + 1) / ranges);
+#pragma unroll 8
+    for (int b = r0; b < r1; ++b) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + static_cast<int64_t>(b) * rf) + q);
+      s4.x += v.x;
+      s4.y += v.y;
+      s4.z += v.z;
+      s4.w += v.w;
+    }
+  }
+  s_red[threadIdx.x] = s4;
+  __syncthreads();
+  float term = 0.f, z_sum = 0.f;
+  if (threadIdx.x < quads) {
+    for (int i = 1; i < ranges; ++i) {
+      const float4 v = s_red[i * quads + q];
+      s4.x += v.x;
+      s4.y += v.y;
+      s4.z += v.z;
+      s4.w += v.w;
+    }
+    if (q == quads - 1) {
+      z_sum = s4.x;
+    } else {
+      const float P[4] = {s4.x * inv_n, s4.y * inv_n, s4.z * inv_n, s4.w * inv_n};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = q * 4 + i;
+        if (e < N) {
+          a.prob_mean[e] = P[i];
+          term += static_cast<float>(s_cnt[e]) * inv_n * P[i];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    term += __shfl_xor_sync(kFull, term, o);
+    z_sum += __shfl_xor_sync(kFull, z_sum, o);
+  }
+  if (lane == 0) {
+    s_z[warp] = z_sum;
+    s_acc[warp][0] = term;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float t = 0.f, z = 0.f;
+    for (int w = 0; w < kBalWarps; ++w) {
+      t += s_acc[w][0];
+      z += s_z[w];
+    }
+    const float balance = a.alpha * static_cast<float>(N) * t;
+    const float zl = a.z_coef * z * inv_n;
+    a.loss[0] = balance + zl;
+    a.loss[1] = balance;
+    a.loss[2] = zl;
+    *a.counter = 0;
+  }
+}
+
+}  // namespace
+
+size_t balance_scratch_bytes(int64_t T, int N, int k) {
+  if (T == 0) return 0;
+  const size_t rows = static_cast<size_t>(count_plan(T, k).rows) * (N + 1) * sizeof(int32_t);
+  return (rows + 15) / 16 * 16 +
+         static_cast<size_t>(balance_ctas(static_cast<int>(T), N, kBalanceMaxCtas)) * row_floats(N) *
+             sizeof(float);
+}
+
+cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
+  DeviceInfo di;
+  cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  const CountPlan cp = count_plan(a.T, a.k);
+  BalanceParams p{};
+  p.logits = a.logits;
+  p.topk_idx = a.topk_idx;
+  p.mask = a.token_mask;
+  p.d_loss = a.d_loss;
+  p.alpha = a.alpha;
+  p.z_coef = a.z_coef;
+  p.counts = a.counts;
+  p.n_tokens = a.n_tokens;
+  p.prob_mean = a.prob_mean;
+  p.loss = a.loss;
+  p.d_logits = a.d_logits;
+  p.count_rows = static_cast<const int32_t*>(a.scratch);
+  p.n_count_rows = cp.rows;
+  p.part = reinterpret_cast<float*>(static_cast<char*>(a.scratch) +
+                                    (static_cast<size_t>(cp.rows) * (a.N + 1) * 4 + 15) / 16 * 16);
+  p.counter = a.counter;
+  p.T = a.T;
+  p.N = a.N;
+  p.k = a.k;
+  if (cp.rows > 0) {
+    e = launch_pdl(balance_count_kernel, dim3(cp.rows), dim3(kBalThreads), 0, s, a.topk_idx,
+                   a.token_mask, static_cast<int32_t*>(a.scratch), a.T, cp.chunk, a.N, a.k);
+    if (e != cudaSuccess) return e;
+  }
+  const TokenShape ts = token_shape(a.N);
+  void (*kern)(BalanceParams) = nullptr;
+  if (ts.vec == 4)
+    kern = ts.g == 4 ? balance_loss_kernel<4, 1, 4> : ts.g == 8 ? balance_loss_kernel<8, 1, 4>
+         : ts.g == 16 ? balance_loss_kernel<16, 1, 4> : ts.c == 1 ? balance_loss_kernel<32, 1, 4>
+         : balance_loss_kernel<32, 2, 4>;
+  else
+    kern = ts.g == 8 ? balance_loss_kernel<8, 1, 1> : ts.g == 16 ? balance_loss_kernel<16, 1, 1>
+         : ts.c == 1 ? balance_loss_kernel<32, 1, 1> : ts.c == 2 ? balance_loss_kernel<32, 2, 1>
+         : ts.c == 4 ? balance_loss_kernel<32, 4, 1> : balance_loss_kernel<32, 8, 1>;
+  const int grid = balance_ctas(a.T, a.N, std::min(di.sm_count, kBalanceMaxCtas));
+  return launch_pdl(kern, dim3(grid), dim3(kBalThreads), 0, s, p);
+}
+
+}  // namespace moe

@@ -301,4 +301,52 @@ struct BackwardArgs {
 size_t backward_router_chunk(int T);
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t s);
 
+// Balance loss and z-loss with their gradient (balance_loss.cu). scratch:
+// balance_scratch_bytes(); counter: an int of the workspace's status region, zero between calls.
+constexpr size_t kBalanceCounterOffset = 132;
+constexpr int kBalanceMaxCtas = 256;  // CTAs (rows of partial sums) at most
+struct BalanceArgs {
+  const float* logits;
+  const int32_t* topk_idx;
+  const uint8_t* token_mask;  // null: every token counts
+  const float* d_loss;        // null: 1
+  float alpha, z_coef;
+  int32_t* counts;
+  int32_t* n_tokens;
+  float* prob_mean;
+  float* loss;
+  float* d_logits;  // null: no gradient
+  void* scratch;
+  int* counter;
+  int T, N, k;
+};
+size_t balance_scratch_bytes(int64_t T, int N, int k);
+cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s);
+
+// Gradient of the linear router for a dense gradient of the logits (router_backward.cu). Null
+// outputs are left out. scratch: router_backward_scratch_bytes().
+struct RouterBackwardArgs {
+  const uint16_t* x;
+  const float* w_router;
+  const float* d_logits;
+  float* d_x;
+  float* d_w_router;
+  float* d_logit_bias;
+  int accumulate;
+  void* scratch;
+  int T, N, d;
+  int* status;
+  uint64_t timeout_ns;
+};
+size_t router_backward_scratch_bytes(int64_t T, int N, int d);
+cudaError_t launch_router_backward(const RouterBackwardArgs& a, cudaStream_t s);
+
+// Gradient norm and AdamW (optimizer.cu). ws: kStatusBytes, then a double for every CTA; the
+// CTAs' arrival counter lies in the status region, zero between calls.
+constexpr int kGradNormSlots = 1024;
+cudaError_t launch_grad_norm(const moe_grad_tensor* tensors, int n, float max_norm, float* norm,
+                             float* scale, void* ws, cudaStream_t s);
+cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int n, const moe_adamw_config& cfg,
+                         cudaStream_t s);
+
 }  // namespace moe
