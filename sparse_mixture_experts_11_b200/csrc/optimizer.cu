@@ -27,6 +27,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -37,6 +38,7 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kOptThreads = 256;
 constexpr int kOptWarps = kOptThreads / 32;
+constexpr int kTileBlocks = 2 * kOptWarps;  // a tile: two blocks for each warp of a CTA
 constexpr int kQBlock = MOE_ADAMW_BLOCK;  // elements of a block: one warp, four a lane
 static_assert(kQBlock == 128, "a warp takes one block, four elements a lane");
 
@@ -181,10 +183,10 @@ struct AdamEntry {
   int32_t chunk0;
   int32_t index;  // place in the caller's list
   float weight_decay;
-  uint8_t params, grad_bf16, bits8, pad;
+  uint8_t params, grad_bf16;
 };
 struct AdamScalars {
-  float lr, b1, omb1, b2, omb2, eps;
+  float lr, b1, omb1, b2, root_b2, root_omb2, eps;  // omb: 1 - beta; root: square roots
   float inv_bc1, inv_sqrt_bc2;  // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
   double beta1, beta2;          // for a step number read on the device
   uint32_t seed;
@@ -195,231 +197,301 @@ struct AdamScalars {
 };
 template <int CAP>
 struct AdamTable {
-  int n, chunks, chunk_blocks;
+  int n, chunks, chunk_tiles;
   AdamEntry e[CAP];
 };
 
 struct StepScalars {  // what every element needs
-  float gs, lr_wd1, step_size, b1, omb1, b2, omb2, inv_sqrt_bc2, eps;
+  float lr_wd1, neg_step, b1, b2;  // 1 - lr wd, -lr / (1 - beta1^t), beta1, beta2 (8 bits: its root)
+  float g1, g2;                    // grad_scale times 1 - beta1 and sqrt(1 - beta2)
+  float inv_sqrt_bc2, eps;
 };
 
+// One special-function operation each, within 2^-23; a v below 2^-126 has root zero.
 __device__ __forceinline__ float sqrt_approx(float x) {
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
-// |x| <= 448 to an E4M3 code, up with the probability of the part that is cut off (u: 16 random
-// bits). E4M3 keeps 3 of fp32's 23 mantissa bits: adding random bits below the cut and
-// truncating rounds so, across binades too. Below 2^-6 the codes are 2^-9 apart, as they are in
-// [2^-6, 2^-5): those values are moved up by 2^-6 and their codes down by 8.
-__device__ __forceinline__ uint32_t e4m3_stochastic(float x, uint32_t u) {
-  float y = fabsf(x);
-  const bool small = y < 0.015625f;
-  y = small ? y + 0.015625f : y;
-  const uint32_t code = ((__float_as_uint(y) + (u << 4) + 8u) >> 20) - (small ? 968u : 960u);
-  return min(code, 126u) | ((__float_as_uint(x) >> 24) & 0x80u);
+// Two fp32 operations in one instruction (sm_100): the kernel is bound by instruction issue where
+// the moments are 8 bits wide, and half of its instructions are fp32 arithmetic.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// E4M3 rounding, up with the probability of the part that is cut off. z = x 2^-120 for |x| <= 448:
+// x = 2^-6, E4M3's smallest normal, becomes 2^-126, fp32's, and the subnormals of the two formats
+// coincide, so the code of x is z's bits above the 20 that E4M3 does not have. Adding 20 random
+// bits (u: 16 of them at bits 4-19) and cutting rounds across binades and into the subnormals
+// alike. Returns the code in bits 24-30; the bits below are noise.
+__device__ __forceinline__ uint32_t e4m3_up(uint32_t z, uint32_t u) {
+  return min(z + u, 0x7EFFFFFu) << 4;
 }
 
 // Four E4M3 codes to fp32 (exact).
-__device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float (&f)[4]) {
+__device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float2 (&f)[2]) {
   uint32_t lo, hi;
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
       "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(w));
-  const float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo));
-  const float2 b = __half22float2(*reinterpret_cast<__half2*>(&hi));
-  f[0] = a.x;
-  f[1] = a.y;
-  f[2] = b.x;
-  f[3] = b.y;
+  f[0] = __half22float2(*reinterpret_cast<__half2*>(&lo));
+  f[1] = __half22float2(*reinterpret_cast<__half2*>(&hi));
 }
 
-// Four consecutive elements from p (16-, 8- or 4-byte aligned when `full`), zeros past `rem`.
-__device__ __forceinline__ void load4(const float* p, bool full, int rem, float (&f)[4]) {
-  if (full) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-    f[0] = a.x;
-    f[1] = a.y;
-    f[2] = a.z;
-    f[3] = a.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = i < rem ? p[i] : 0.f;
-  }
+// Four consecutive elements as loaded: fp32 in 16 bytes, bf16 in 8, codes in 4. Elements past
+// `rem` read as zero and are not written; FULL: there are four.
+template <bool FULL>
+__device__ __forceinline__ uint4 load_f32x4(const float* p, int rem) {
+  if (FULL || rem >= 4) return __ldcs(reinterpret_cast<const uint4*>(p));
+  uint4 a = make_uint4(0u, 0u, 0u, 0u);
+  if (rem > 0) a.x = __float_as_uint(p[0]);
+  if (rem > 1) a.y = __float_as_uint(p[1]);
+  if (rem > 2) a.z = __float_as_uint(p[2]);
+  return a;
 }
-__device__ __forceinline__ void load4(const uint16_t* p, bool full, int rem, float (&f)[4]) {
-  if (full) {
-    const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p));
-    f[0] = __uint_as_float(a.x << 16);
-    f[1] = __uint_as_float(a.x & 0xffff0000u);
-    f[2] = __uint_as_float(a.y << 16);
-    f[3] = __uint_as_float(a.y & 0xffff0000u);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = i < rem ? bf16_bits_to_float(p[i]) : 0.f;
-  }
+template <bool FULL>
+__device__ __forceinline__ uint2 load_bf16x4(const uint16_t* p, int rem) {
+  if (FULL || rem >= 4) return __ldcs(reinterpret_cast<const uint2*>(p));
+  uint2 a = make_uint2(0u, 0u);
+  if (rem > 0) a.x = p[0];
+  if (rem > 1) a.x |= static_cast<uint32_t>(p[1]) << 16;
+  if (rem > 2) a.y = p[2];
+  return a;
 }
-__device__ __forceinline__ uint32_t load4(const uint8_t* p, bool full, int rem) {
-  if (full) return __ldcs(reinterpret_cast<const uint32_t*>(p));
+template <bool FULL>
+__device__ __forceinline__ uint32_t load_u8x4(const uint8_t* p, int rem) {
+  if (FULL || rem >= 4) return __ldcs(reinterpret_cast<const uint32_t*>(p));
   uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < rem) w |= static_cast<uint32_t>(p[i]) << (8 * i);
+  if (rem > 0) w = p[0];
+  if (rem > 1) w |= static_cast<uint32_t>(p[1]) << 8;
+  if (rem > 2) w |= static_cast<uint32_t>(p[2]) << 16;
   return w;
 }
-__device__ __forceinline__ void store4(float* p, bool full, int rem, const float (&f)[4]) {
-  if (full) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+__device__ __forceinline__ void unpack(const uint4& a, float2 (&f)[2]) {
+  f[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+  f[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+}
+__device__ __forceinline__ void unpack(const uint2& a, float2 (&f)[2]) {
+  f[0] = make_float2(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u));
+  f[1] = make_float2(__uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u));
+}
+template <bool FULL>
+__device__ __forceinline__ void store4(float* p, int rem, const float2 (&f)[2]) {
+  if (FULL || rem >= 4) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0].x, f[0].y, f[1].x, f[1].y));
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < rem) p[i] = f[i];
+    if (rem > 0) p[0] = f[0].x;
+    if (rem > 1) p[1] = f[0].y;
+    if (rem > 2) p[2] = f[1].x;
   }
 }
-__device__ __forceinline__ void store4(uint16_t* p, bool full, int rem, uint32_t lo, uint32_t hi) {
-  if (full) {
+template <bool FULL>
+__device__ __forceinline__ void store4(uint16_t* p, int rem, uint32_t lo, uint32_t hi) {
+  if (FULL || rem >= 4) {
     __stcs(reinterpret_cast<uint2*>(p), make_uint2(lo, hi));
   } else {
-    const uint32_t w[2] = {lo, hi};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < rem) p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    if (rem > 0) p[0] = static_cast<uint16_t>(lo);
+    if (rem > 1) p[1] = static_cast<uint16_t>(lo >> 16);
+    if (rem > 2) p[2] = static_cast<uint16_t>(hi);
   }
 }
-__device__ __forceinline__ void store4(uint8_t* p, bool full, int rem, uint32_t w) {
-  if (full) {
+template <bool FULL>
+__device__ __forceinline__ void store4(uint8_t* p, int rem, uint32_t w) {
+  if (FULL || rem >= 4) {
     __stcs(reinterpret_cast<uint32_t*>(p), w);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 3; ++i)
       if (i < rem) p[i] = static_cast<uint8_t>(w >> (8 * i));
   }
 }
 
-// One warp, U consecutive blocks of a tensor from block b0 (those below b1 exist). Lane l takes
-// elements 4 l .. 4 l + 3 of each block: 16-byte accesses to fp32, one cache line a warp to the
-// codes, and a block's amax is one warp reduction. All loads of the U blocks are issued first.
-template <int PARAMS, bool GRAD_BF16, bool BITS8, int U>
-__device__ __forceinline__ void adam_blocks(const AdamEntry& t, const StepScalars& s, uint32_t key,
-                                            int64_t b0, int64_t b1, int lane) {
-  float p[U][4], g[U][4], m[U][4], v[U][4], ms[U], vs[U];
-  uint32_t mq[U], vq[U];
-  int rem[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t i = (b0 + u) * kQBlock + lane * 4;
-    const int64_t left = t.numel - i;
-    rem[u] = b0 + u < b1 && left > 0 ? static_cast<int>(min(left, static_cast<int64_t>(4))) : 0;
-    const bool full = rem[u] == 4;
-    if (PARAMS == kFp32) load4(static_cast<const float*>(t.param) + i, full, rem[u], p[u]);
-    else if (PARAMS == kMaster) load4(t.master + i, full, rem[u], p[u]);
-    else load4(static_cast<const uint16_t*>(t.param) + i, full, rem[u], p[u]);
-    if (GRAD_BF16) load4(static_cast<const uint16_t*>(t.grad) + i, full, rem[u], g[u]);
-    else load4(static_cast<const float*>(t.grad) + i, full, rem[u], g[u]);
-    if (BITS8) {
-      mq[u] = load4(static_cast<const uint8_t*>(t.m) + i, full, rem[u]);
-      vq[u] = load4(static_cast<const uint8_t*>(t.v) + i, full, rem[u]);
-      ms[u] = b0 + u < b1 ? t.m_scale[b0 + u] : 0.f;
-      vs[u] = b0 + u < b1 ? t.v_scale[b0 + u] : 0.f;
-    } else {
-      load4(static_cast<const float*>(t.m) + i, full, rem[u], m[u]);
-      load4(static_cast<const float*>(t.v) + i, full, rem[u], v[u]);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (b0 + u >= b1) break;  // warp-uniform
-    const int64_t i = (b0 + u) * kQBlock + lane * 4;
-    const bool full = rem[u] == 4;
-    float r[4];
-    if (BITS8) {
-      e4m3x4_to_float(mq[u], m[u]);
-      e4m3x4_to_float(vq[u], v[u]);
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (BITS8) {
-        m[u][q] *= ms[u];
-        v[u][q] *= vs[u];
-        v[u][q] *= v[u][q];
-      }
-      const float gv = g[u][q] * s.gs;
-      m[u][q] = s.b1 * m[u][q] + s.omb1 * gv;
-      v[u][q] = s.b2 * v[u][q] + s.omb2 * gv * gv;
-      r[q] = sqrt_approx(v[u][q]);
-      p[u][q] = p[u][q] * s.lr_wd1 -
-                s.step_size * __fdividef(m[u][q], r[q] * s.inv_sqrt_bc2 + s.eps);
-    }
-    uint32_t h[4];
-    if (BITS8 || PARAMS == kAlone) {
-      const uint32_t base = static_cast<uint32_t>(i) * 0x9E3779B1u + key +
-                            static_cast<uint32_t>(i >> 32) * 0x85EBCA6Bu;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) h[q] = mix32(base + q * 0x9E3779B1u);
-    }
-    if (PARAMS == kFp32) {
-      store4(static_cast<float*>(t.param) + i, full, rem[u], p[u]);
-    } else if (PARAMS == kMaster) {
-      store4(t.master + i, full, rem[u], p[u]);
-      store4(static_cast<uint16_t*>(t.param) + i, full, rem[u], pack_bf16x2(p[u][0], p[u][1]),
-             pack_bf16x2(p[u][2], p[u][3]));
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        w[q] = __float_as_uint(p[u][q]) + ((h[q] * 0xD1B54A35u + key) >> 16);
-      store4(static_cast<uint16_t*>(t.param) + i, full, rem[u], __byte_perm(w[0], w[1], 0x7632),
-             __byte_perm(w[2], w[3], 0x7632));
-    }
-    if (BITS8) {
-      uint32_t ma = 0, ra = 0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        ma = max(ma, __float_as_uint(fabsf(m[u][q])));
-        ra = max(ra, __float_as_uint(r[q]));
-      }
-      ma = __reduce_max_sync(kFull, ma);
-      ra = __reduce_max_sync(kFull, ra);
-      // a block below 2^-96 (its reciprocal would overflow) is kept as zeros
-      const float m_max = __uint_as_float(ma) < 0x1p-96f ? 0.f : __uint_as_float(ma);
-      const float r_max = __uint_as_float(ra) < 0x1p-96f ? 0.f : __uint_as_float(ra);
-      const float m_inv = m_max > 0.f ? 448.f / m_max : 0.f;
-      const float r_inv = r_max > 0.f ? 448.f / r_max : 0.f;
-      uint32_t mw = 0, rw = 0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t mc = m_max > 0.f ? e4m3_stochastic(m[u][q] * m_inv, h[q] & 0xffffu) : 0u;
-        uint32_t rc = r_max > 0.f ? e4m3_stochastic(r[q] * r_inv, h[q] >> 16) : 0u;
-        if (r_max > 0.f && r[q] > 0.f) rc = max(rc, 1u);
-        mw |= mc << (8 * q);
-        rw |= rc << (8 * q);
-      }
-      store4(static_cast<uint8_t*>(t.m) + i, full, rem[u], mw);
-      store4(static_cast<uint8_t*>(t.v) + i, full, rem[u], rw);
-      if (lane == 0) {
-        t.m_scale[b0 + u] = m_max * (1.0f / 448.0f);
-        t.v_scale[b0 + u] = r_max * (1.0f / 448.0f);
-      }
-    } else {
-      store4(static_cast<float*>(t.m) + i, full, rem[u], m[u]);
-      store4(static_cast<float*>(t.v) + i, full, rem[u], v[u]);
-    }
-  }
+template <bool FULL>
+__device__ __forceinline__ void load4(const void* p, int64_t i, int rem, uint4& a) {
+  a = load_f32x4<FULL>(static_cast<const float*>(p) + i, rem);
+}
+template <bool FULL>
+__device__ __forceinline__ void load4(const void* p, int64_t i, int rem, uint2& a) {
+  a = load_bf16x4<FULL>(static_cast<const uint16_t*>(p) + i, rem);
 }
 
+// A lane's four elements of one block, as loaded: elements 4 l .. 4 l + 3 for lane l, so that fp32
+// takes 16-byte accesses, the codes one cache line a warp, and a block's amax one warp reduction.
 template <int PARAMS, bool GRAD_BF16, bool BITS8>
-__device__ __forceinline__ void adam_chunk(const AdamEntry& t, const StepScalars& s, uint32_t key,
-                                           int64_t b0, int64_t b1) {
-  constexpr int U = 2;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int64_t b = b0 + warp * U; b < b1; b += kOptWarps * U)
-    adam_blocks<PARAMS, GRAD_BF16, BITS8, U>(t, s, key, b, b1, lane);
+struct Work {
+  std::conditional_t<PARAMS == kAlone, uint2, uint4> p;
+  std::conditional_t<GRAD_BF16, uint2, uint4> g;
+  uint4 m, v;         // fp32 moments
+  uint32_t m8, v8;    // or codes
+  float ms, vs;       // and scales
+  template <bool FULL>
+  __device__ __forceinline__ void load(const AdamEntry& t, int64_t b, int64_t i, int rem) {
+    load4<FULL>(PARAMS == kMaster ? t.master : t.param, i, rem, p);
+    load4<FULL>(t.grad, i, rem, g);
+    if (BITS8) {
+      m8 = load_u8x4<FULL>(static_cast<const uint8_t*>(t.m) + i, rem);
+      v8 = load_u8x4<FULL>(static_cast<const uint8_t*>(t.v) + i, rem);
+      ms = t.m_scale[b];
+      vs = t.v_scale[b];
+    } else {
+      load4<FULL>(t.m, i, rem, m);
+      load4<FULL>(t.v, i, rem, v);
+    }
+  }
+};
+
+// The step on one block b, by a warp; i: the lane's first element. FULL: the block is whole, else
+// only `rem` of the lane's elements exist.
+template <int PARAMS, bool GRAD_BF16, bool BITS8, bool FULL>
+__device__ __forceinline__ void adam_block(const AdamEntry& t, const StepScalars& s, uint32_t key,
+                                           int64_t b, int64_t i, int rem, int lane,
+                                           const Work<PARAMS, GRAD_BF16, BITS8>& w) {
+  float2 p[2], g[2], m[2], v[2], r[2];
+  unpack(w.p, p);
+  unpack(w.g, g);
+  if (BITS8) {
+    e4m3x4_to_float(w.m8, m);
+    e4m3x4_to_float(w.v8, v);
+  } else {
+    unpack(w.m, m);
+    unpack(w.v, v);
+  }
+  // (1 - beta2) g'^2, and beta2 v where v is held as its root, are squares of scaled roots: the
+  // constants go into the scales
+  const float ms = BITS8 ? w.ms * s.b1 : s.b1, vs = BITS8 ? w.vs * s.b2 : s.b2;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float2 g2 = mul2(g[q], both(s.g2));
+    m[q] = fma2(m[q], both(ms), mul2(g[q], both(s.g1)));
+    const float2 v_old = mul2(v[q], both(vs));
+    v[q] = BITS8 ? fma2(v_old, v_old, mul2(g2, g2)) : fma2(g2, g2, v_old);
+    r[q] = make_float2(sqrt_approx(v[q].x), sqrt_approx(v[q].y));
+    const float2 den = fma2(r[q], both(s.inv_sqrt_bc2), both(s.eps));
+    const float2 upd = mul2(mul2(m[q], both(s.neg_step)),
+                            make_float2(rcp_approx(den.x), rcp_approx(den.y)));
+    p[q] = fma2(p[q], both(s.lr_wd1), upd);
+  }
+  uint32_t h[4];
+  if (BITS8 || PARAMS == kAlone) {
+    const uint32_t base = static_cast<uint32_t>(i) * 0x9E3779B1u + key +
+                          static_cast<uint32_t>(i >> 32) * 0x85EBCA6Bu;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) h[q] = mix32(base + q * 0x9E3779B1u);
+  }
+  if (PARAMS == kFp32) {
+    store4<FULL>(static_cast<float*>(t.param) + i, rem, p);
+  } else if (PARAMS == kMaster) {
+    store4<FULL>(t.master + i, rem, p);
+    store4<FULL>(static_cast<uint16_t*>(t.param) + i, rem, pack_bf16x2(p[0].x, p[0].y),
+                 pack_bf16x2(p[1].x, p[1].y));
+  } else {
+    const float pv[4] = {p[0].x, p[0].y, p[1].x, p[1].y};
+    uint32_t up[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) up[q] = __float_as_uint(pv[q]) + ((h[q] * 0xD1B54A35u + key) >> 16);
+    store4<FULL>(static_cast<uint16_t*>(t.param) + i, rem, __byte_perm(up[0], up[1], 0x7632),
+                 __byte_perm(up[2], up[3], 0x7632));
+  }
+  if (BITS8) {
+    const float ma4 = fmaxf(fmaxf(fabsf(m[0].x), fabsf(m[0].y)), fmaxf(fabsf(m[1].x), fabsf(m[1].y)));
+    const float ra4 = fmaxf(fmaxf(r[0].x, r[0].y), fmaxf(r[1].x, r[1].y));
+    const float ma = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(ma4)));
+    const float ra = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(ra4)));
+    // a block below 2^-96 (its reciprocal could overflow) is kept as zeros: codes and scale
+    const float m_max = ma < 0x1p-96f ? 0.f : ma, r_max = ra < 0x1p-96f ? 0.f : ra;
+    const float m_inv = m_max > 0.f ? 448.f * rcp_approx(m_max) : 0.f;
+    const float r_inv = r_max > 0.f ? 448.f * rcp_approx(r_max) : 0.f;
+    const uint32_t least = r_max > 0.f ? 1u << 24 : 0u;  // a nonzero r's smallest code
+    uint32_t mc[4], rc[4];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float2 mz = mul2(mul2(m[q], both(m_inv)), both(0x1p-120f));
+      const float2 rz = mul2(mul2(r[q], both(r_inv)), both(0x1p-120f));
+      const float mzv[2] = {mz.x, mz.y}, rzv[2] = {rz.x, rz.y}, rv[2] = {r[q].x, r[q].y};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t hw = h[2 * q + j], mb = __float_as_uint(mzv[j]);
+        // rounding leaves a zero zero: the random bits alone never reach a code
+        mc[2 * q + j] = (e4m3_up(mb & 0x7fffffffu, ((hw << 4) & 0xffff0u) + 8u) & 0x7fffffffu) |
+                        (mb & 0x80000000u);
+        rc[2 * q + j] = max(e4m3_up(__float_as_uint(rzv[j]), ((hw >> 12) & 0xffff0u) + 8u),
+                            min(__float_as_uint(rv[j]), least));
+      }
+    }
+    store4<FULL>(static_cast<uint8_t*>(t.m) + i, rem,
+                 __byte_perm(__byte_perm(mc[0], mc[1], 0x0073), __byte_perm(mc[2], mc[3], 0x0073), 0x5410));
+    store4<FULL>(static_cast<uint8_t*>(t.v) + i, rem,
+                 __byte_perm(__byte_perm(rc[0], rc[1], 0x0073), __byte_perm(rc[2], rc[3], 0x0073), 0x5410));
+    if (lane == 0) {
+      t.m_scale[b] = m_max * (1.0f / 448.0f);
+      t.v_scale[b] = r_max * (1.0f / 448.0f);
+    }
+  } else {
+    store4<FULL>(static_cast<float*>(t.m) + i, rem, m);
+    store4<FULL>(static_cast<float*>(t.v) + i, rem, v);
+  }
 }
 
-template <int CAP>
-__global__ void __launch_bounds__(kOptThreads)
+// A tensor's last block, when it is not whole, by the warp whose turn it is.
+template <int PARAMS, bool GRAD_BF16, bool BITS8>
+__device__ __forceinline__ void adam_rest(const AdamEntry& t, const StepScalars& s, uint32_t key,
+                                          int64_t b, int lane) {
+  const int64_t i = b * kQBlock + lane * 4;
+  const int rem = static_cast<int>(max(min(t.numel - i, static_cast<int64_t>(4)), static_cast<int64_t>(0)));
+  Work<PARAMS, GRAD_BF16, BITS8> w;
+  w.template load<false>(t, b, i, rem);
+  adam_block<PARAMS, GRAD_BF16, BITS8, false>(t, s, key, b, i, rem, lane, w);
+}
+
+// Tiles [tile, tile + n) of a tensor; a warp takes two blocks of each, their loads issued together.
+// Only the tensor's last tile can be short.
+template <int PARAMS, bool GRAD_BF16, bool BITS8>
+__device__ __forceinline__ void adam_run(const AdamEntry& t, const StepScalars& s, int64_t tile,
+                                         int n, uint32_t key) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t whole = t.numel / kQBlock;
+  int64_t b = tile * kTileBlocks + warp * 2;
+  for (; n > 0; --n, b += kTileBlocks) {
+    const int64_t i = b * kQBlock + lane * 4;
+    if (b + 2 <= whole) {
+      Work<PARAMS, GRAD_BF16, BITS8> w[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) w[u].template load<true>(t, b + u, i + u * kQBlock, 4);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        adam_block<PARAMS, GRAD_BF16, BITS8, true>(t, s, key, b + u, i + u * kQBlock, 4, lane, w[u]);
+    } else {
+      for (int64_t c = b; c < b + 2 && c * kQBlock < t.numel; ++c)
+        adam_rest<PARAMS, GRAD_BF16, BITS8>(t, s, key, c, lane);
+    }
+  }
+}
+
+// BITS8: the table holds tensors with 8-bit moments, else with fp32 ones (two kernels: the
+// conversions of the one would cost the other its registers).
+template <bool BITS8, int CAP>
+__global__ void __launch_bounds__(kOptThreads, BITS8 ? 4 : 3)
     adamw_kernel(const __grid_constant__ AdamTable<CAP> tab, const AdamScalars sc) {
   __shared__ float s_bc[2];
   pdl_trigger();
@@ -442,28 +514,33 @@ __global__ void __launch_bounds__(kOptThreads)
   const float lr = sc.lr_dev != nullptr ? *sc.lr_dev : sc.lr;
   for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
     const AdamEntry& t = tab.e[find_entry(tab.e, tab.n, c)];
-    const int64_t blocks = (t.numel + kQBlock - 1) / kQBlock;
-    const int64_t b0 = static_cast<int64_t>(c - t.chunk0) * tab.chunk_blocks;
-    const int64_t b1 = min(blocks, b0 + tab.chunk_blocks);
-    const StepScalars s{gs,      1.0f - lr * t.weight_decay, lr * inv_bc1, sc.b1, sc.omb1, sc.b2,
-                        sc.omb2, inv_sqrt_bc2,               sc.eps};
+    const int64_t tile = static_cast<int64_t>(c - t.chunk0) * tab.chunk_tiles;
+    const int64_t tiles = (t.numel - 1) / (kTileBlocks * kQBlock) + 1;
+    const int n = static_cast<int>(min(tiles - tile, static_cast<int64_t>(tab.chunk_tiles)));
+    const StepScalars s{1.0f - lr * t.weight_decay, -lr * inv_bc1,     sc.b1,        BITS8 ? sc.root_b2 : sc.b2,
+                        gs * sc.omb1,               gs * sc.root_omb2, inv_sqrt_bc2, sc.eps};
     const uint32_t key =
         mix32(mix32(static_cast<uint32_t>(t.index) * 0x632BE5ABu + sc.seed) +
               static_cast<uint32_t>(step) * 0x9E3779B1u);
     // uniform over the CTA
-    switch ((t.params * 2 + t.grad_bf16) * 2 + t.bits8) {
-      case 0: adam_chunk<kFp32, false, false>(t, s, key, b0, b1); break;
-      case 1: adam_chunk<kFp32, false, true>(t, s, key, b0, b1); break;
-      case 2: adam_chunk<kFp32, true, false>(t, s, key, b0, b1); break;
-      case 3: adam_chunk<kFp32, true, true>(t, s, key, b0, b1); break;
-      case 4: adam_chunk<kMaster, false, false>(t, s, key, b0, b1); break;
-      case 5: adam_chunk<kMaster, false, true>(t, s, key, b0, b1); break;
-      case 6: adam_chunk<kMaster, true, false>(t, s, key, b0, b1); break;
-      case 7: adam_chunk<kMaster, true, true>(t, s, key, b0, b1); break;
-      case 8: adam_chunk<kAlone, false, false>(t, s, key, b0, b1); break;
-      case 9: adam_chunk<kAlone, false, true>(t, s, key, b0, b1); break;
-      case 10: adam_chunk<kAlone, true, false>(t, s, key, b0, b1); break;
-      default: adam_chunk<kAlone, true, true>(t, s, key, b0, b1); break;
+    if (BITS8) {
+      switch (t.params * 2 + t.grad_bf16) {
+        case 0: adam_run<kFp32, false, true>(t, s, tile, n, key); break;
+        case 1: adam_run<kFp32, true, true>(t, s, tile, n, key); break;
+        case 2: adam_run<kMaster, false, true>(t, s, tile, n, key); break;
+        case 3: adam_run<kMaster, true, true>(t, s, tile, n, key); break;
+        case 4: adam_run<kAlone, false, true>(t, s, tile, n, key); break;
+        default: adam_run<kAlone, true, true>(t, s, tile, n, key); break;
+      }
+    } else {
+      switch (t.params * 2 + t.grad_bf16) {
+        case 0: adam_run<kFp32, false, false>(t, s, tile, n, key); break;
+        case 1: adam_run<kFp32, true, false>(t, s, tile, n, key); break;
+        case 2: adam_run<kMaster, false, false>(t, s, tile, n, key); break;
+        case 3: adam_run<kMaster, true, false>(t, s, tile, n, key); break;
+        case 4: adam_run<kAlone, false, false>(t, s, tile, n, key); break;
+        default: adam_run<kAlone, true, false>(t, s, tile, n, key); break;
+      }
     }
   }
 }
@@ -471,6 +548,59 @@ __global__ void __launch_bounds__(kOptThreads)
 constexpr int kAdamTable = 384;  // entries of one launch: 30 KB of kernel parameters
 static_assert(sizeof(AdamTable<kAdamTable>) + sizeof(AdamScalars) <= 32764, "kernel parameters");
 static_assert(sizeof(NormTable) + 64 <= 32764, "kernel parameters");
+
+// The tensors of one kind (8-bit or fp32 moments) of the list, kAdamTable a launch.
+template <bool BITS8>
+cudaError_t launch_adamw_kind(const moe_adamw_tensor* tensors, int n, const AdamScalars& sc, int sms,
+                              cudaStream_t s) {
+  auto kern = adamw_kernel<BITS8, kAdamTable>;
+  int64_t total = 0;  // tiles
+  for (int i = 0; i < n; ++i)
+    if (tensors[i].numel > 0 && (tensors[i].state_bits == 8) == BITS8)
+      total += (tensors[i].numel - 1) / (kTileBlocks * kQBlock) + 1;
+  if (total == 0) return cudaSuccess;
+  // fp32 moments: a CTA a tile, in the tensor's order. What bounds the kernel is how well the
+  // memory streams, and CTAs that start in order keep all SMs within a few pages of each other
+  // (537M elements with masters: 2308 us; persistent CTAs on chunks of 16 tiles, 2550 us).
+  // 8 bits: as many CTAs as are resident, on chunks that grow with the total: here instructions
+  // bound, and a CTA's start is half of a tile's (1514 us; a CTA a tile, 1691 us).
+  const int64_t resident = static_cast<int64_t>(sms) * 4;
+  int chunk_tiles = 1;
+  while (BITS8 && chunk_tiles < 32 && total / chunk_tiles > 8 * resident) chunk_tiles *= 2;
+  AdamTable<kAdamTable> tab;
+  for (int i = 0; i < n;) {
+    tab.n = 0;
+    tab.chunk_tiles = chunk_tiles;
+    int64_t chunks = 0;
+    for (; i < n && tab.n < kAdamTable; ++i) {
+      const moe_adamw_tensor& in = tensors[i];
+      if (in.numel == 0 || (in.state_bits == 8) != BITS8) continue;
+      const int64_t c = ((in.numel - 1) / (kTileBlocks * kQBlock) + chunk_tiles) / chunk_tiles;
+      if (chunks + c > INT32_MAX) return cudaErrorInvalidValue;
+      AdamEntry& t = tab.e[tab.n++];
+      t.param = in.param;
+      t.master = in.master;
+      t.grad = in.grad;
+      t.m = in.m;
+      t.v = in.v;
+      t.m_scale = in.m_scale;
+      t.v_scale = in.v_scale;
+      t.numel = in.numel;
+      t.chunk0 = static_cast<int32_t>(chunks);
+      t.index = i;
+      t.weight_decay = in.weight_decay;
+      t.params = in.param_dtype == MOE_DTYPE_F32 ? kFp32 : in.master != nullptr ? kMaster : kAlone;
+      t.grad_bf16 = in.grad_dtype == MOE_DTYPE_BF16;
+      chunks += c;
+    }
+    if (chunks == 0) break;
+    tab.chunks = static_cast<int>(chunks);
+    const int grid = static_cast<int>(BITS8 ? std::min<int64_t>(chunks, resident) : chunks);
+    const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kOptThreads), 0, s, tab, sc);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 }  // namespace
 
@@ -526,7 +656,8 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int n, const moe_adamw
   sc.b1 = static_cast<float>(cfg.beta1);
   sc.omb1 = static_cast<float>(1.0 - cfg.beta1);
   sc.b2 = static_cast<float>(cfg.beta2);
-  sc.omb2 = static_cast<float>(1.0 - cfg.beta2);
+  sc.root_b2 = static_cast<float>(sqrt(cfg.beta2));
+  sc.root_omb2 = static_cast<float>(sqrt(1.0 - cfg.beta2));
   sc.eps = static_cast<float>(cfg.eps);
   sc.beta1 = cfg.beta1;
   sc.beta2 = cfg.beta2;
@@ -539,48 +670,8 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int n, const moe_adamw
   sc.step_dev = cfg.step_dev;
   sc.lr_dev = cfg.lr_dev;
   sc.grad_scale = cfg.grad_scale;
-  int64_t total = 0;
-  for (int i = 0; i < n; ++i) total += (tensors[i].numel + kQBlock - 1) / kQBlock;
-  const int64_t resident = static_cast<int64_t>(di.sm_count) * 8;
-  // blocks of a chunk: one pass of the CTA's warps (16 blocks) while that leaves fewer chunks
-  // than CTAs, up to eight passes for large totals
-  int chunk_blocks = 16;
-  while (chunk_blocks < 128 && total / chunk_blocks > resident) chunk_blocks *= 2;
-  AdamTable<kAdamTable> tab;
-  for (int i = 0; i < n;) {
-    tab.n = 0;
-    tab.chunk_blocks = chunk_blocks;
-    int64_t chunks = 0;
-    for (; i < n && tab.n < kAdamTable; ++i) {
-      const moe_adamw_tensor& in = tensors[i];
-      if (in.numel == 0) continue;
-      const int64_t c = ((in.numel + kQBlock - 1) / kQBlock + chunk_blocks - 1) / chunk_blocks;
-      if (chunks + c > INT32_MAX) return cudaErrorInvalidValue;
-      AdamEntry& t = tab.e[tab.n++];
-      t.param = in.param;
-      t.master = in.master;
-      t.grad = in.grad;
-      t.m = in.m;
-      t.v = in.v;
-      t.m_scale = in.m_scale;
-      t.v_scale = in.v_scale;
-      t.numel = in.numel;
-      t.chunk0 = static_cast<int32_t>(chunks);
-      t.index = i;
-      t.weight_decay = in.weight_decay;
-      t.params = in.param_dtype == MOE_DTYPE_F32 ? kFp32 : in.master != nullptr ? kMaster : kAlone;
-      t.grad_bf16 = in.grad_dtype == MOE_DTYPE_BF16;
-      t.bits8 = in.state_bits == 8;
-      t.pad = 0;
-      chunks += c;
-    }
-    if (chunks == 0) break;
-    tab.chunks = static_cast<int>(chunks);
-    const int grid = static_cast<int>(std::min<int64_t>(chunks, resident));
-    e = launch_pdl(adamw_kernel<kAdamTable>, dim3(grid), dim3(kOptThreads), 0, s, tab, sc);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  e = launch_adamw_kind<false>(tensors, n, sc, di.sm_count, s);
+  return e != cudaSuccess ? e : launch_adamw_kind<true>(tensors, n, sc, di.sm_count, s);
 }
 
 }  // namespace moe

@@ -218,7 +218,8 @@ def check_router(T, d, N, x, w, g, outs, old, which):
 
 ROUTER_CASES = [(1, 64, 1), (1, 128, 256), (3, 64, 5), (64, 128, 8), (65, 192, 7), (130, 2880, 32),
                 (257, 1024, 64), (512, 448, 130), (1000, 320, 33), (700, 7168, 17), (4096, 1024, 64),
-                (2049, 640, 256), (5000, 256, 100), (16384, 512, 31), (8192, 4096, 8)]
+                (2049, 640, 256), (5000, 256, 100), (16384, 512, 31), (8192, 4096, 8),
+                (2001, 2880, 7), (1537, 448, 130), (300, 576, 200), (16384, 64, 256), (260, 4096, 40)]
 
 
 @pytest.mark.parametrize("T,d,N", ROUTER_CASES)
@@ -358,7 +359,13 @@ def check_adamw(before, t, kind, **hyper):
         assert (np.abs(after["m"] - want["m"]) <= m_tol).all()
         assert (np.abs(after["v"] - want["v"]) <= 8 * U * want["v"] + 1e-44).all()
     else:
-        np.testing.assert_allclose(after["m_scale"], want["m_scale"], rtol=10 * U, atol=0)
+        # the scale is the largest |m'| of the block / 448, and m' is known to m_tol, not to a part of
+        # itself: b1 m and (1 - b1) g may cancel (a block of one element did, to 1e-3 of either).
+        # The magnitudes' errors bound that of their maximum; the product with 1 / 448 rounds twice
+        pad = np.zeros(len(want["m_scale"]) * 128)
+        pad[:n] = m_tol
+        s_tol = pad.reshape(-1, 128).max(1) / 448 + 4 * U * want["m_scale"]
+        assert (np.abs(after["m_scale"] - want["m_scale"]) <= s_tol).all()
         np.testing.assert_allclose(after["v_scale"], want["v_scale"], rtol=10 * U, atol=0)
         for name in ("m", "v"):
             differ = after[name] != want[name]
