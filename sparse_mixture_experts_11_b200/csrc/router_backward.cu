@@ -10,6 +10,8 @@
 
 #include <algorithm>
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "launch.h"
 #include "tma_host.h"
@@ -177,47 +179,78 @@ __global__ void __launch_bounds__(kThreads) router_backward_kernel(const Params 
   else x_tile(a, s_dl);
 }
 
-// The token ranges' partial sums, added in order.
+// The token ranges' partial sums, added in order (CTAs [0, w_ctas): four elements of dW_r a thread);
+// the bias gradient's by a warp an expert, 32 strided sums and their tree.
 __global__ void __launch_bounds__(256) router_backward_sum_kernel(
     const float* __restrict__ part_w, const float* __restrict__ part_b, float* __restrict__ d_w,
-    float* __restrict__ d_b, int chunks, int b_parts, int N, int d, int accumulate) {
+    float* __restrict__ d_b, int chunks, int b_parts, int N, int d, int accumulate, int w_ctas) {
   pdl_trigger();
   pdl_wait();
+  if (static_cast<int>(blockIdx.x) >= w_ctas) {
+    const int n = (blockIdx.x - w_ctas) * 8 + threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (n >= N) return;
+    float s = 0.f;
+#pragma unroll 4
+    for (int c = lane; c < b_parts; c += 32) s += part_b[static_cast<int64_t>(c) * N + n];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+    if (lane == 0) d_b[n] = accumulate ? d_b[n] + s : s;
+    return;
+  }
   const int64_t items = static_cast<int64_t>(N) * d / 4;
   const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-  if (d_w != nullptr && i < items) {
-    float4 s = accumulate ? reinterpret_cast<const float4*>(d_w)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+  if (i >= items) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int c = 0; c < chunks; ++c) {
-      const float4 v = reinterpret_cast<const float4*>(part_w)[c * items + i];
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
-    reinterpret_cast<float4*>(d_w)[i] = s;
+  for (int c = 0; c < chunks; ++c) {
+    const float4 v = reinterpret_cast<const float4*>(part_w)[c * items + i];
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
   }
-  if (d_b != nullptr && i < N) {
-    float s = accumulate ? d_b[i] : 0.f;
-#pragma unroll 8
-    for (int c = 0; c < b_parts; ++c) s += part_b[static_cast<int64_t>(c) * N + i];
-    d_b[i] = s;
+  float4* out = reinterpret_cast<float4*>(d_w) + i;
+  if (accumulate) {
+    const float4 old = *out;
+    s.x += old.x;
+    s.y += old.y;
+    s.z += old.z;
+    s.w += old.w;
   }
+  *out = s;
+}
+
+cudaError_t launch_sum(const float* part_w, const float* part_b, const RouterBackwardArgs& a, int chunks,
+                       int b_parts, cudaStream_t s) {
+  const int64_t items = static_cast<int64_t>(a.N) * a.d / 4;
+  const int w_ctas = a.d_w_router != nullptr ? static_cast<int>((items + 255) / 256) : 0;
+  const int b_ctas = a.d_logit_bias != nullptr ? (a.N + 7) / 8 : 0;
+  return launch_pdl(router_backward_sum_kernel, dim3(w_ctas + b_ctas), dim3(256), 0, s, part_w, part_b,
+                    a.d_w_router, a.d_logit_bias, chunks, b_parts, a.N, a.d, a.accumulate, w_ctas);
 }
 
 // ------------------------------------------------------------------ tensor-core path
-// An fp32 number is the sum of three bf16 terms (8 significant bits each). dL^T x with x exact in
-// bf16 takes three products; dL W_r takes the six whose size reaches 2^-16 of the leading one
-// (those left out are below 2^-24). The terms are written once, by split_kernel, and both GEMMs
-// put the axis d on the 128 rows of the MMA: the accumulator's lanes then run along the
-// contiguous axis of the outputs, and a warp's 32 lanes store 128 consecutive bytes straight
+// Both products have fp32 operands, which are written once as sums of 16-bit terms:
+//   dL^T x   x is exactly bf16, so dL is three bf16 terms (24 bits): three products;
+//   dL W_r   both are two fp16 terms (22 bits) after scaling by powers of two, exact: row n of W_r
+//            by 2^(14 - b_n), b_n the exponent of its largest magnitude, and dL[t, n] by
+//            2^(14 + b_n - a_t), a_t that of the largest dL[t, n] 2^(b_n). Three products (the
+//            fourth is below 2^-22); the result of token t is scaled back by 2^(a_t - 28). Three bf16
+//            terms of each would need six products.
+// The accumulator of the MMA truncates: measured, a chain of additions loses 1.1e-8 of its value a
+// step of 16 products. dx has 3 N / 16 <= 48 steps. dW's chains would be thousands; they are cut
+// after 48 steps (kFlush stages) and summed in fp32 registers by the epilogue warps, while the
+// other half of TMEM takes the next chain.
+// Both GEMMs put the axis d on the 128 rows of the MMA: the accumulator's lanes then run along
+// the contiguous axis of the outputs, and a warp's 32 lanes store 128 consecutive bytes straight
 // from registers.
-constexpr int kKb = 32;           // reduction elements of a stage
+constexpr int kKb = 32;             // reduction elements of a stage
 constexpr int kBox = 64 * kKb * 2;  // one TMA box of an MN-major operand: 64 MN x 32 k, 128B-swizzled
-constexpr int kTcThreads = 320;   // TMA producer, MMA issuer, eight epilogue warps
+constexpr int kTcThreads = 320;     // TMA producer, MMA issuer, eight epilogue warps
 constexpr int kTcMinSmem = 120 * 1024;  // one CTA an SM: the TMEM is not shared
-constexpr int kTcMaxSmem = 227 * 1024;
-constexpr int kWTile = 256;       // columns of d a CTA of the weight gradient owns (two MMA row blocks)
+constexpr int kTcMaxSmem = 226 * 1024;  // dynamic; barriers beside it
+constexpr int kWTile = 256;         // columns of d a CTA of the weight gradient owns (two MMA row blocks)
+constexpr int kFlush = 8;           // stages of a chain: 8 * 2 steps * 3 terms = 48
 constexpr int kXTileC = 128, kXTileT = 256;
 
 // Shared-memory descriptor of an MN-major operand of kKb k rows: groups of 8 k rows are 1024 bytes
@@ -226,104 +259,187 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
   return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(kBox >> 4) << 16) |
          (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-// K-major operand with 64-byte rows (32 bf16, 64B-swizzled): groups of 8 rows are 512 bytes.
+// K-major operand with 64-byte rows (32 elements, 64B-swizzled): groups of 8 rows are 512 bytes.
 __device__ __forceinline__ uint64_t desc_k64(uint32_t addr) {
   return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (1ull << 16) |
          (static_cast<uint64_t>(512u >> 4) << 32) | (1ull << 46) | (4ull << 61);
 }
 
 struct TcPlan {
-  int np;       // N rounded up to 8: row length of the terms of dL
-  int nu;       // N rounded up to 16: MMA columns of the weight gradient
-  int n_boxes;  // boxes of 64 experts
-  int c_tiles, chunks;
+  int np;  // N rounded up to 8: row length of dL's terms
+  int nu;  // experts of a weight-gradient tile (MMA columns): 16, 32, 64 or 128
+  int n_tiles, c_tiles, chunks;
   int64_t chunk;  // tokens of a range of the weight gradient, a multiple of kKb
-  int w_stages, w_stage_bytes;
-  int split_rows, split_ctas;  // tokens a CTA of split_kernel takes, and how many such CTAs
-  size_t dl_bytes, w_bytes, part_bytes, bias_bytes;
+  int split_rows, split_ctas;  // tokens a CTA of split_dl_kernel takes, and how many such CTAs
+  size_t dl16_bytes, dl_bytes, w_bytes, exp_bytes, part_bytes, bias_bytes;
+  size_t total() const { return dl16_bytes + dl_bytes + w_bytes + exp_bytes + part_bytes + bias_bytes; }
 };
+__host__ __device__ constexpr int w_stage_bytes(int nu) { return (kWTile / 64 + 3 * ((nu + 63) / 64)) * kBox; }
+__host__ __device__ constexpr int w_stages(int nu) {
+  return (kTcMaxSmem - 1024) / w_stage_bytes(nu) < 8 ? (kTcMaxSmem - 1024) / w_stage_bytes(nu) : 8;
+}
 
 TcPlan make_tc_plan(int64_t T, int N, int d) {
   TcPlan p{};
   p.np = (N + 7) / 8 * 8;
-  p.nu = (N + 15) / 16 * 16;
-  p.n_boxes = (N + 63) / 64;
+  p.nu = N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : 128;
+  p.n_tiles = (N + p.nu - 1) / p.nu;
   p.c_tiles = (d + kWTile - 1) / kWTile;
-  const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>(148 / p.c_tiles, T / 128));
-  p.chunk = ((T + chunks - 1) / chunks + kKb - 1) / kKb * kKb;
+  // Token ranges: the fewest tokens a CTA in all (whole waves of 148 CTAs), where starting and
+  // ending a CTA costs about what 128 tokens do
+  const int64_t tiles = static_cast<int64_t>(p.n_tiles) * p.c_tiles;
+  int64_t best = 0;
+  for (int64_t c = 1; c <= 32 && (c == 1 || T / c >= 256); ++c) {
+    const int64_t len = ((T + c - 1) / c + kKb - 1) / kKb * kKb;
+    const int64_t cost = (tiles * c + 147) / 148 * (len + 128);
+    if (best == 0 || cost < best) {
+      best = cost;
+      p.chunk = len;
+    }
+  }
   p.chunks = static_cast<int>((T + p.chunk - 1) / p.chunk);
-  p.w_stage_bytes = (kWTile / 64 + 3 * p.n_boxes) * kBox;
-  p.w_stages = std::min(8, (kTcMaxSmem - 2048) / p.w_stage_bytes);
-  p.split_rows = static_cast<int>(std::max<int64_t>(8, (T + 295) / 296));
+  p.split_rows = static_cast<int>(std::max<int64_t>(8, (T + 591) / 592));
   p.split_ctas = static_cast<int>((T + p.split_rows - 1) / p.split_rows);
   auto r256 = [](size_t v) { return (v + 255) / 256 * 256; };
+  p.dl16_bytes = r256(static_cast<size_t>(2) * T * p.np * 2);
   p.dl_bytes = r256(static_cast<size_t>(3) * T * p.np * 2);
-  p.w_bytes = r256(static_cast<size_t>(3) * N * d * 2);
+  p.w_bytes = r256(static_cast<size_t>(2) * N * d * 2);
+  p.exp_bytes = r256(static_cast<size_t>(N) * 4) + r256(static_cast<size_t>(T) * 4);
   p.part_bytes = r256(static_cast<size_t>(p.chunks) * N * d * 4);
   p.bias_bytes = r256(static_cast<size_t>(p.split_ctas) * N * 4);
   return p;
 }
 
-__device__ __forceinline__ void split3(float v, uint16_t& hi, uint16_t& mid, uint16_t& lo) {
+__device__ __forceinline__ uint16_t bf16_term(float& v) {
   const __nv_bfloat16 h = __float2bfloat16_rn(v);
-  const float r = v - __bfloat162float(h);
-  const __nv_bfloat16 m = __float2bfloat16_rn(r);
-  const __nv_bfloat16 l = __float2bfloat16_rn(r - __bfloat162float(m));
-  hi = __bfloat16_as_ushort(h);
-  mid = __bfloat16_as_ushort(m);
-  lo = __bfloat16_as_ushort(l);
+  v -= __bfloat162float(h);
+  return __bfloat16_as_ushort(h);
+}
+__device__ __forceinline__ uint16_t fp16_term(float& v) {
+  const __half h = __float2half_rn(v);
+  v -= __half2float(h);
+  return __half_as_ushort(h);
+}
+// e with 2^(e-1) <= |v| < 2^e; 0 for zero
+__device__ __forceinline__ int exponent_of(float v) {
+  int e = 0;
+  frexpf(v, &e);
+  return e;
 }
 
-// CTAs [0, split_ctas): dL's terms [3][T][np] and the bias gradient's partial sums of their tokens;
-// the others: W_r's terms [3][N][d].
-__global__ void __launch_bounds__(kThreads) split_kernel(const float* __restrict__ dl,
-                                                         const float* __restrict__ w,
-                                                         uint16_t* __restrict__ dl_terms,
-                                                         uint16_t* __restrict__ w_terms,
-                                                         float* __restrict__ bias_part, int64_t T,
-                                                         int N, int np, int64_t w_items, int rows,
-                                                         int dl_ctas) {
+// CTA n: row n of W_r as two fp16 terms [2][N][d], scaled by 2^(14 - b_n), and b_n.
+__global__ void __launch_bounds__(kThreads) split_w_kernel(const float* __restrict__ w,
+                                                           uint16_t* __restrict__ terms,
+                                                           int32_t* __restrict__ w_exp, int N, int d) {
+  __shared__ float s_max[kThreads / 32];
   pdl_trigger();
   pdl_wait();
-  if (static_cast<int>(blockIdx.x) >= dl_ctas) {
-    const int64_t plane = w_items;
-    for (int64_t i = ((blockIdx.x - dl_ctas) * static_cast<int64_t>(kThreads) + threadIdx.x) * 4; i < w_items;
-         i += static_cast<int64_t>(gridDim.x - dl_ctas) * kThreads * 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(w + i));
-      const float f[4] = {v.x, v.y, v.z, v.w};
-      uint16_t t[3][4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) split3(f[q], t[0][q], t[1][q], t[2][q]);
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        *reinterpret_cast<uint2*>(w_terms + k * plane + i) =
-            make_uint2(t[k][0] | static_cast<uint32_t>(t[k][1]) << 16, t[k][2] | static_cast<uint32_t>(t[k][3]) << 16);
-    }
-    return;
+  const float4* src = reinterpret_cast<const float4*>(w + static_cast<int64_t>(blockIdx.x) * d);
+  float m = 0.f;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < d / 4; i += kThreads) {
+    const float4 v = __ldg(src + i);
+    m = fmaxf(m, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
   }
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * rows;
-  const int n_rows = static_cast<int>(min(static_cast<int64_t>(rows), T - t0));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, s_max[i]);
+  const int b = exponent_of(m);
+  if (threadIdx.x == 0) w_exp[blockIdx.x] = b;
+  uint16_t* out = terms + static_cast<int64_t>(blockIdx.x) * d;
+  const int64_t plane = static_cast<int64_t>(N) * d;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < d / 4; i += kThreads) {
+    const float4 v4 = __ldg(src + i);
+    float v[4] = {scalbnf(v4.x, 14 - b), scalbnf(v4.y, 14 - b), scalbnf(v4.z, 14 - b), scalbnf(v4.w, 14 - b)};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint16_t t[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) t[q] = fp16_term(v[q]);
+      *reinterpret_cast<uint2*>(out + k * plane + 4 * i) =
+          make_uint2(t[0] | static_cast<uint32_t>(t[1]) << 16, t[2] | static_cast<uint32_t>(t[3]) << 16);
+    }
+  }
+}
+
+// A warp a token: dL's row as two scaled fp16 terms [2][T][np] with a_t (for dx; w_exp null: left
+// out) and as three bf16 terms [3][T][np] (for dW; dl_terms null: left out); the CTA's sums over its
+// tokens for the bias.
+__global__ void __launch_bounds__(kThreads) split_dl_kernel(
+    const float* __restrict__ dl, const int32_t* __restrict__ w_exp, uint16_t* __restrict__ dl16,
+    int32_t* __restrict__ row_exp, uint16_t* __restrict__ dl_terms, float* __restrict__ bias_part, int64_t T,
+    int N, int np, int rows) {
+  __shared__ float s_sum[kThreads / 32][256];
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * rows, t1 = min(T, t0 + rows);
   const int64_t plane = T * np;
-  const int pairs = np / 2;
-  for (int i = threadIdx.x; i < n_rows * pairs; i += kThreads) {
-    const int r = i / pairs, n = i % pairs * 2;
-    const float* src = dl + (t0 + r) * N + n;
-    const float a = n < N ? src[0] : 0.f, b = n + 1 < N ? src[1] : 0.f;
-    uint16_t ta[3], tb[3];
-    split3(a, ta[0], ta[1], ta[2]);
-    split3(b, tb[0], tb[1], tb[2]);
+  float acc[8];
+  int b[8];
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
-      *reinterpret_cast<uint32_t*>(dl_terms + k * plane + (t0 + r) * np + n) =
-          ta[k] | static_cast<uint32_t>(tb[k]) << 16;
+  for (int j = 0; j < 4; ++j) {
+    // values 2 j, 2 j + 1 of this lane: experts j * 64 + lane * 2 and the next
+    const int n = j * 64 + lane * 2;
+    acc[2 * j] = acc[2 * j + 1] = 0.f;
+    b[2 * j] = w_exp != nullptr && n < N ? w_exp[n] : 0;
+    b[2 * j + 1] = w_exp != nullptr && n + 1 < N ? w_exp[n + 1] : 0;
   }
-  if (bias_part != nullptr) {
-    for (int n = threadIdx.x; n < N; n += kThreads) {
-      float s = 0.f;
-#pragma unroll 8
-      for (int r = 0; r < n_rows; ++r) s += dl[(t0 + r) * N + n];
-      bias_part[static_cast<int64_t>(blockIdx.x) * N + n] = s;
+  for (int64_t t = t0 + warp; t < t1; t += kThreads / 32) {
+    float v[8];
+    int top = -1000;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = j * 64 + lane * 2;
+      v[2 * j] = n < N ? dl[t * N + n] : 0.f;
+      v[2 * j + 1] = n + 1 < N ? dl[t * N + n + 1] : 0.f;
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      acc[j] += v[j];
+      if (v[j] != 0.f) top = max(top, exponent_of(v[j]) + b[j]);
+    }
+    if (w_exp != nullptr) {
+      top = __reduce_max_sync(kFull, top);
+      if (lane == 0) row_exp[t] = top;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = j * 64 + lane * 2;
+        if (n >= np) break;
+        float x = scalbnf(v[2 * j], 14 + b[2 * j] - top), y = scalbnf(v[2 * j + 1], 14 + b[2 * j + 1] - top);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t lo = fp16_term(x), hi = fp16_term(y);
+          *reinterpret_cast<uint32_t*>(dl16 + k * plane + t * np + n) = lo | hi << 16;
+        }
+      }
+    }
+    if (dl_terms != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = j * 64 + lane * 2;
+        if (n >= np) break;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const uint32_t lo = bf16_term(v[2 * j]), hi = bf16_term(v[2 * j + 1]);
+          *reinterpret_cast<uint32_t*>(dl_terms + k * plane + t * np + n) = lo | hi << 16;
+        }
+      }
+    }
+  }
+  if (bias_part == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s_sum[warp][j / 2 * 64 + lane * 2 + j % 2] = acc[j];
+  __syncthreads();
+  for (int n = threadIdx.x; n < N; n += kThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) s += s_sum[w][n];
+    bias_part[static_cast<int64_t>(blockIdx.x) * N + n] = s;
   }
 }
 
@@ -338,7 +454,7 @@ struct TcShared {
 };
 
 // Barriers and TMEM of a CTA; columns: a power of two.
-__device__ __forceinline__ void tc_setup(TcShared& sh, int warp, uint32_t columns, int epilogue_threads) {
+__device__ __forceinline__ void tc_setup(TcShared& sh, int warp, uint32_t columns) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&sh.full[i]), 1);
@@ -346,7 +462,7 @@ __device__ __forceinline__ void tc_setup(TcShared& sh, int warp, uint32_t column
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.tfull[i]), 1);
-      mbar_init(smem_u32(&sh.tempty[i]), epilogue_threads);
+      mbar_init(smem_u32(&sh.tempty[i]), kTcThreads - 64);
     }
     mbar_init(smem_u32(&sh.done), 1);
     sh.abort = 0;
@@ -361,80 +477,96 @@ __device__ __forceinline__ void tc_setup(TcShared& sh, int warp, uint32_t column
   tc_fence_after_sync();
 }
 
-// Weight gradient: one CTA for 256 columns of d and one range of the tokens. A: x [t][c], MN-major,
-// two row blocks of 128 columns; B: the terms of dL [t][n], MN-major; D[c][n] in TMEM, columns
-// [0, nu) and [nu, 2 nu). The sum over the range goes to part [chunk][N][d].
+// Weight gradient: one CTA for 256 columns of d, NU experts and one range of the tokens. A: x [t][c],
+// MN-major, two row blocks of 128 columns; B: the terms of dL [t][n], MN-major. D[c][n]: two chains
+// in TMEM, buffer u at columns [2 NU u, 2 NU (u + 1)), row block m at + NU m. The range's sum goes to
+// part [range][N][d].
+template <int NU>
 __global__ void __launch_bounds__(kTcThreads, 1)
     router_wgrad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_dl,
-                        float* __restrict__ part, int64_t T, int N, int d, int nu, int n_boxes, int c_tiles,
-                        int64_t chunk, int stages, uint32_t columns, int* status, uint64_t timeout_ns) {
+                        float* __restrict__ part, int64_t T, int N, int d, int c_tiles, int n_tiles, int64_t chunk,
+                        int* status, uint64_t timeout_ns) {
+  constexpr int kStages = w_stages(NU), kStageBytes = w_stage_bytes(NU), kBoxes = (NU + 63) / 64;
+  constexpr uint32_t kColumns = 4 * NU;
   extern __shared__ __align__(1024) uint8_t dyn_smem[];
   __shared__ TcShared sh;
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(dyn_smem) + 1023u) & ~1023u;
-  tc_setup(sh, warp, columns, kTcThreads - 64);
+  tc_setup(sh, warp, kColumns);
   pdl_wait();
   const uint32_t tmem = sh.tmem;
-  const int c0 = static_cast<int>(blockIdx.x) % c_tiles * kWTile;
-  const int range = static_cast<int>(blockIdx.x) / c_tiles;
+  // neighbouring CTAs share a range and columns of x
+  const int n0 = static_cast<int>(blockIdx.x) % n_tiles * NU;
+  const int c0 = static_cast<int>(blockIdx.x) / n_tiles % c_tiles * kWTile;
+  const int range = static_cast<int>(blockIdx.x) / (n_tiles * c_tiles);
   const int64_t t0 = range * chunk, t1 = min(T, t0 + chunk);
   const int nkb = static_cast<int>((t1 - t0 + kKb - 1) / kKb);
   const int a_boxes = min(kWTile / 64, (d - c0) / 64);  // d is a multiple of 64
-  const int stage_bytes = (kWTile / 64 + 3 * n_boxes) * kBox;
   if (warp == 0) {
     if (lane == 0) {
-      const uint64_t first = l2_policy_evict_first(), last = l2_policy_evict_last();
+      const uint64_t last = l2_policy_evict_last();
       int it = 0;
       bool ok = true;
       for (; it < nkb; ++it) {
-        const int s = it % stages;
-        if (!mbar_wait(smem_u32(&sh.empty[s]), ((it / stages) & 1) ^ 1u, timeout_ns, &sh.abort)) {
+        const int s = it % kStages;
+        if (!mbar_wait(smem_u32(&sh.empty[s]), ((it / kStages) & 1) ^ 1u, timeout_ns, &sh.abort)) {
           ok = false;
           break;
         }
         const uint32_t fb = smem_u32(&sh.full[s]);
-        const uint32_t dst = base + s * stage_bytes, b_dst = dst + kWTile / 64 * kBox;
+        const uint32_t dst = base + s * kStageBytes, b_dst = dst + kWTile / 64 * kBox;
         const int t = static_cast<int>(t0) + it * kKb;
-        mbar_arrive_expect_tx(fb, (a_boxes + 3 * n_boxes) * kBox);
-        for (int i = 0; i < a_boxes; ++i) tma_load_2d(dst + i * kBox, &tm_x, fb, c0 + 64 * i, t, first);
+        mbar_arrive_expect_tx(fb, (a_boxes + 3 * kBoxes) * kBox);
+        for (int i = 0; i < a_boxes; ++i) tma_load_2d(dst + i * kBox, &tm_x, fb, c0 + 64 * i, t, last);
+#pragma unroll
         for (int k = 0; k < 3; ++k)
-          for (int i = 0; i < n_boxes; ++i)
-            tma_load_3d(b_dst + (k * n_boxes + i) * kBox, &tm_dl, fb, 64 * i, t, k, last);
+#pragma unroll
+          for (int i = 0; i < kBoxes; ++i)
+            tma_load_3d(b_dst + (k * kBoxes + i) * kBox, &tm_dl, fb, n0 + 64 * i, t, k, last);
       }
       if (!ok) {
         sh.abort = 1;
         report_error(status, MOE_ERR_TIMEOUT);
       }
-      for (int i = max(0, it - stages); i < it; ++i)  // no copy is still landing when the CTA exits
-        mbar_wait(smem_u32(&sh.full[i % stages]), (i / stages) & 1, kDrainTimeoutNs, nullptr);
+      for (int i = max(0, it - kStages); i < it; ++i)  // no copy is still landing when the CTA exits
+        mbar_wait(smem_u32(&sh.full[i % kStages]), (i / kStages) & 1, kDrainTimeoutNs, nullptr);
     }
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_bf16_f32(128, nu) | (1u << 15) | (1u << 16);
+    constexpr uint32_t idesc = idesc_bf16_f32(128, NU) | (1u << 15) | (1u << 16);
     const int blocks = (a_boxes + 1) / 2;  // row blocks of 128 columns
     bool ok = true, issued = false;
     for (int it = 0; it < nkb; ++it) {
-      const int s = it % stages;
-      const bool got = mbar_wait(smem_u32(&sh.full[s]), (it / stages) & 1, timeout_ns, &sh.abort);
+      const int s = it % kStages, u = it / kFlush;
+      if (it % kFlush == 0) {
+        const bool free_buf = mbar_wait(smem_u32(&sh.tempty[u & 1]), ((u >> 1) & 1) ^ 1u, timeout_ns, &sh.abort);
+        if (!__all_sync(kFull, free_buf)) {
+          ok = false;
+          break;
+        }
+      }
+      const bool got = mbar_wait(smem_u32(&sh.full[s]), (it / kStages) & 1, timeout_ns, &sh.abort);
       if (!__all_sync(kFull, got)) {
         ok = false;
         break;
       }
       tc_fence_after_sync();
       if (lane == 0) {
-        const uint32_t a = base + s * stage_bytes, b = a + kWTile / 64 * kBox;
+        const uint32_t a = base + s * kStageBytes, b = a + kWTile / 64 * kBox;
+        const uint32_t dst = tmem + (u & 1) * 2 * NU;
         for (int m = 0; m < blocks; ++m)
+#pragma unroll
           for (int kk = 0; kk < kKb / 16; ++kk)
 #pragma unroll
             for (int k = 0; k < 3; ++k)
-              tc_mma_f16(tmem + m * nu, desc_mn(a + 2 * m * kBox + kk * 2048),
-                         desc_mn(b + k * n_boxes * kBox + kk * 2048), idesc, it > 0 || kk > 0 || k > 0);
+              tc_mma_f16(dst + m * NU, desc_mn(a + 2 * m * kBox + kk * 2048),
+                         desc_mn(b + k * kBoxes * kBox + kk * 2048), idesc, it % kFlush > 0 || kk > 0 || k > 0);
         tc_commit(smem_u32(&sh.empty[s]));
+        if (it % kFlush == kFlush - 1 || it == nkb - 1) tc_commit(smem_u32(&sh.tfull[u & 1]));
       }
       issued = true;
       __syncwarp();
     }
-    if (ok && lane == 0) tc_commit(smem_u32(&sh.tfull[0]));
     if (!ok && lane == 0) {
       sh.abort = 1;
       report_error(status, MOE_ERR_TIMEOUT);
@@ -444,55 +576,72 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_wait(smem_u32(&sh.done), 0, kDrainTimeoutNs, nullptr);
     }
   } else {
-    const int q = warp & 3;           // TMEM lane quadrant
-    const int m = (warp - 2) >> 2;    // row block
+    const int q = warp & 3;               // TMEM lane quadrant
+    const int m = (warp - 2) >> 2;        // row block
     const int c = c0 + m * 128 + q * 32;  // the warp's first column of d; 32-column groups are whole
-    const bool got = mbar_wait(smem_u32(&sh.tfull[0]), 0, timeout_ns, &sh.abort);
-    if (!__all_sync(kFull, got)) {
+    float acc[NU];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) acc[i] = 0.f;
+    const uint32_t row = tmem + (static_cast<uint32_t>(q * 32) << 16) + m * NU;
+    bool ok = true;
+    for (int u = 0; u * kFlush < nkb; ++u) {
+      const bool got = mbar_wait(smem_u32(&sh.tfull[u & 1]), (u >> 1) & 1, timeout_ns, &sh.abort);
+      if (!__all_sync(kFull, got)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      if (c < d) {
+#pragma unroll
+        for (int n = 0; n < NU; n += 16) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(row + (u & 1) * 2 * NU + n, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[n + i] += __uint_as_float(v[i]);
+        }
+      }
+      tc_fence_before_sync();
+      mbar_arrive(smem_u32(&sh.tempty[u & 1]));
+    }
+    if (!ok) {
       sh.abort = 1;
       report_error(status, MOE_ERR_TIMEOUT);
     } else if (c < d) {
-      tc_fence_after_sync();
-      float* out = part + static_cast<int64_t>(range) * N * d + c + lane;
-      const uint32_t row = tmem + (static_cast<uint32_t>(q * 32) << 16) + m * nu;
-      for (int n = 0; n < nu; n += 16) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(row + n, v);
-        tmem_ld_wait();
+      float* out = part + (static_cast<int64_t>(range) * N + n0) * d + c + lane;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (n + i < N) out[static_cast<int64_t>(n + i) * d] = __uint_as_float(v[i]);
-      }
+      for (int i = 0; i < NU; ++i)
+        if (n0 + i < N) out[static_cast<int64_t>(i) * d] = acc[i];
     }
   }
   tc_fence_before_sync();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, columns);
+    tmem_dealloc(tmem, kColumns);
   }
 }
 
 // dx: persistent CTAs over tiles of 128 columns of d x 256 tokens. A: W_r's terms [n][c], MN-major;
-// B: dL's terms [t][n], K-major; six products a k step into D[c][t]; two accumulators, so one
+// B: dL's terms [t][n], K-major; three products a k step into D[c][t]; two accumulators, so one
 // tile's epilogue runs beside the next one's MMAs. Accumulating adds in the L2 (a reduction
 // without a return: one addition an element, so the order is fixed, and no SM waits for the old
 // values).
-constexpr int kXStages = 3;
-constexpr int kXStageBytes = 3 * 2 * kBox + 3 * kXTileT * kKb * 2;
+constexpr int kXStages = 4;
+constexpr int kXStageBytes = 2 * 2 * kBox + 2 * kXTileT * kKb * 2;
 constexpr int kXSmem = kXStages * kXStageBytes + 1024;
-static_assert(kXSmem + 1024 <= kTcMaxSmem, "shared memory");
+static_assert(kXSmem <= kTcMaxSmem, "shared memory");
 
 __global__ void __launch_bounds__(kTcThreads, 1)
     router_dgrad_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_dl,
-                        float* __restrict__ d_x, int64_t T, int N, int d, int c_tiles, int64_t tiles,
-                        int accumulate, int* status, uint64_t timeout_ns) {
+                        const int32_t* __restrict__ row_exp, float* __restrict__ d_x, int64_t T, int N, int d,
+                        int c_tiles, int64_t tiles, int accumulate, int* status, uint64_t timeout_ns) {
   extern __shared__ __align__(1024) uint8_t dyn_smem[];
   __shared__ TcShared sh;
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(dyn_smem) + 1023u) & ~1023u;
-  tc_setup(sh, warp, 512, kTcThreads - 64);
+  tc_setup(sh, warp, 512);
   pdl_wait();
   const uint32_t tmem = sh.tmem;
   const int nkb = (N + kKb - 1) / kKb;
@@ -512,9 +661,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             break;
           }
           const uint32_t fb = smem_u32(&sh.full[s]);
-          const uint32_t a = base + s * kXStageBytes, b = a + 3 * 2 * kBox;
-          mbar_arrive_expect_tx(fb, 3 * (a_boxes * kBox + kXTileT * kKb * 2));
-          for (int k = 0; k < 3; ++k) {
+          const uint32_t a = base + s * kXStageBytes, b = a + 2 * 2 * kBox;
+          mbar_arrive_expect_tx(fb, 2 * (a_boxes * kBox + kXTileT * kKb * 2));
+          for (int k = 0; k < 2; ++k) {
             for (int i = 0; i < a_boxes; ++i)
               tma_load_3d(a + (2 * k + i) * kBox, &tm_w, fb, c0 + 64 * i, kb * kKb, k, last);
             tma_load_3d(b + k * (kXTileT * kKb * 2), &tm_dl, fb, kb * kKb, r0, k, last);
@@ -529,7 +678,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_wait(smem_u32(&sh.full[i % kXStages]), (i / kXStages) & 1, kDrainTimeoutNs, nullptr);
     }
   } else if (warp == 1) {
-    constexpr uint32_t idesc = idesc_bf16_f32(kXTileC, kXTileT) | (1u << 15);  // A MN-major, B K-major
+    // fp16 operands (formats 0), A MN-major, B K-major
+    constexpr uint32_t idesc = (1u << 4) | (1u << 15) | (static_cast<uint32_t>(kXTileT >> 3) << 17) |
+                               (static_cast<uint32_t>(kXTileC >> 4) << 24);
     bool ok = true, issued = false;
     int it = 0, uc = 0;
     for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++uc) {
@@ -549,16 +700,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         tc_fence_after_sync();
         if (lane == 0) {
-          const uint32_t a = base + s * kXStageBytes, b = a + 3 * 2 * kBox;
+          const uint32_t a = base + s * kXStageBytes, b = a + 2 * 2 * kBox;
           const int steps = min(kKb / 16, (N - kb * kKb + 15) / 16);
           for (int kk = 0; kk < steps; ++kk)
 #pragma unroll
-            for (int ka = 0; ka < 3; ++ka)
-#pragma unroll
-              for (int kt = 0; kt + ka < 3; ++kt)
-                tc_mma_f16(tmem + buf * kXTileT, desc_mn(a + 2 * ka * kBox + kk * 2048),
-                           desc_k64(b + kt * (kXTileT * kKb * 2) + kk * 32), idesc,
-                           kb > 0 || kk > 0 || ka > 0 || kt > 0);
+            for (int k = 0; k < 3; ++k)  // terms (0, 0), (0, 1), (1, 0)
+              tc_mma_f16(tmem + buf * kXTileT, desc_mn(a + (k == 2 ? 2 * kBox : 0) + kk * 2048),
+                         desc_k64(b + (k == 1 ? kXTileT * kKb * 2 : 0) + kk * 32), idesc, kb > 0 || kk > 0 || k > 0);
           tc_commit(smem_u32(&sh.empty[s]));
         }
         issued = true;
@@ -576,11 +724,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_wait(smem_u32(&sh.done), 0, kDrainTimeoutNs, nullptr);
     }
   } else {
-    const int q = warp & 3;                  // TMEM lane quadrant: columns q * 32 .. of the tile
-    const int half = (warp - 2) >> 2;        // tokens [half * 128, half * 128 + 128) of the tile
+    const int q = warp & 3;            // TMEM lane quadrant: columns q * 32 .. of the tile
+    const int half = (warp - 2) >> 2;  // tokens [half * 128, half * 128 + 128) of the tile
     int uc = 0;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++uc) {
       const int buf = uc & 1;
+      const int c = static_cast<int>(t % c_tiles) * kXTileC + q * 32;
+      const int64_t r0 = t / c_tiles * kXTileT + half * 128;
+      float scale[4];  // 2^(a_t) of tokens r0 + 32 j + lane
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        scale[j] = r0 + 32 * j + lane < T ? scalbnf(1.0f, max(-126, min(127, row_exp[r0 + 32 * j + lane]))) : 0.f;
       const bool got = mbar_wait(smem_u32(&sh.tfull[buf]), (uc >> 1) & 1, timeout_ns, &sh.abort);
       if (!__all_sync(kFull, got)) {
         sh.abort = 1;
@@ -588,24 +742,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         break;
       }
       tc_fence_after_sync();
-      const int c = static_cast<int>(t % c_tiles) * kXTileC + q * 32;
-      const int64_t r0 = t / c_tiles * kXTileT + half * 128;
       const uint32_t row = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * kXTileT + half * 128;
       if (c < d) {
-        for (int j = 0; j < 128 && r0 + j < T; j += 32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (r0 + 32 * j >= T) break;  // warp-uniform
           uint32_t v[32];
-          tmem_ld_32x32b_x32(row + j, v);
+          tmem_ld_32x32b_x32(row + 32 * j, v);
           tmem_ld_wait();
-          float* out = d_x + (r0 + j) * d + c + lane;
-          const int rows = static_cast<int>(min(static_cast<int64_t>(32), T - r0 - j));
-          if (accumulate) {
+          float* out = d_x + (r0 + 32 * j) * d + c + lane;
+          const int rows = static_cast<int>(min(static_cast<int64_t>(32), T - r0 - 32 * j));
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < rows) atomicAdd(out + static_cast<int64_t>(i) * d, __uint_as_float(v[i]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < rows) __stcs(out + static_cast<int64_t>(i) * d, __uint_as_float(v[i]));
+          for (int i = 0; i < 32; ++i) {
+            const float r = __uint_as_float(v[i]) * 0x1p-28f * __shfl_sync(kFull, scale[j], i);
+            if (i < rows) {
+              if (accumulate) atomicAdd(out + static_cast<int64_t>(i) * d, r);
+              else __stcs(out + static_cast<int64_t>(i) * d, r);
+            }
           }
         }
       }
@@ -624,74 +777,89 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // Tensor cores where the products are worth the five launches.
 bool use_tensor_cores(int64_t T, int N, int d) { return T >= 256 && static_cast<double>(T) * N * d >= kTcWork; }
 
+template <int NU>
+cudaError_t launch_wgrad(const CUtensorMap& mx, const CUtensorMap& mdl, float* part, const RouterBackwardArgs& a,
+                         const TcPlan& p, cudaStream_t s) {
+  constexpr int smem = std::max(kTcMinSmem, w_stages(NU) * w_stage_bytes(NU) + 1024);
+  static PerDeviceOnce once;
+  const cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(router_wgrad_kernel<NU>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(router_wgrad_kernel<NU>, dim3(p.n_tiles * p.c_tiles * p.chunks), dim3(kTcThreads), smem, s, mx,
+                    mdl, part, static_cast<int64_t>(a.T), a.N, a.d, p.c_tiles, p.n_tiles, p.chunk, a.status,
+                    a.timeout_ns);
+}
+
 cudaError_t launch_tc(const RouterBackwardArgs& a, cudaStream_t s) {
   const TcPlan p = make_tc_plan(a.T, a.N, a.d);
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
   char* ws = static_cast<char*>(a.scratch);
-  uint16_t* dl_terms = reinterpret_cast<uint16_t*>(ws);
-  uint16_t* w_terms = reinterpret_cast<uint16_t*>(ws + p.dl_bytes);
-  float* part = reinterpret_cast<float*>(ws + p.dl_bytes + p.w_bytes);
-  float* bias_part = reinterpret_cast<float*>(ws + p.dl_bytes + p.w_bytes + p.part_bytes);
+  auto take = [&ws](size_t bytes) {
+    char* r = ws;
+    ws += bytes;
+    return r;
+  };
+  uint16_t* dl16 = reinterpret_cast<uint16_t*>(take(p.dl16_bytes));
+  uint16_t* dl_terms = reinterpret_cast<uint16_t*>(take(p.dl_bytes));
+  uint16_t* w_terms = reinterpret_cast<uint16_t*>(take(p.w_bytes));
+  int32_t* row_exp = reinterpret_cast<int32_t*>(take(p.exp_bytes));  // [T], then [N]
+  int32_t* w_exp = row_exp + (static_cast<int64_t>(a.T) + 63) / 64 * 64;
+  float* part = reinterpret_cast<float*>(take(p.part_bytes));
+  float* bias_part = reinterpret_cast<float*>(take(p.bias_bytes));
   const uint64_t T = static_cast<uint64_t>(a.T), d = static_cast<uint64_t>(a.d), np = static_cast<uint64_t>(p.np);
-  {
-    const int64_t w_items = a.d_x != nullptr ? static_cast<int64_t>(a.N) * a.d : 0;
-    const int w_ctas = static_cast<int>(std::min<int64_t>((w_items / 4 + kThreads - 1) / kThreads, 592));
-    e = launch_pdl(split_kernel, dim3(p.split_ctas + w_ctas), dim3(kThreads), 0, s, a.d_logits, a.w_router,
-                   dl_terms, w_terms, a.d_logit_bias != nullptr ? bias_part : nullptr,
-                   static_cast<int64_t>(a.T), a.N, p.np, w_items, p.split_rows, p.split_ctas);
+  const bool want_x = a.d_x != nullptr, want_w = a.d_w_router != nullptr, want_b = a.d_logit_bias != nullptr;
+  if (want_x) {
+    e = launch_pdl(split_w_kernel, dim3(a.N), dim3(kThreads), 0, s, a.w_router, w_terms, w_exp, a.N, a.d);
     if (e != cudaSuccess) return e;
   }
-  const uint64_t dl_dims[3] = {np, T, 3}, dl_str[2] = {np * 2, T * np * 2};
-  static PerDeviceOnce once;
-  e = once.run([] {
-    const cudaError_t r = cudaFuncSetAttribute(router_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMaxSmem - 1024);
-    return r != cudaSuccess ? r : cudaFuncSetAttribute(router_dgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kXSmem);
-  });
+  e = launch_pdl(split_dl_kernel, dim3(p.split_ctas), dim3(kThreads), 0, s, a.d_logits,
+                 want_x ? static_cast<const int32_t*>(w_exp) : nullptr, dl16, row_exp, want_w ? dl_terms : nullptr,
+                 want_b ? bias_part : nullptr, static_cast<int64_t>(a.T), a.N, p.np, p.split_rows);
   if (e != cudaSuccess) return e;
-  if (a.d_w_router != nullptr) {
+  if (want_w) {
     CUtensorMap mx, mdl;
-    const uint64_t xd[2] = {d, T}, xs[1] = {d * 2};
-    const uint32_t xb[2] = {64, kKb}, db[3] = {64, kKb, 1};
-    if (!make_map(&mx, a.x, 2, xd, xs, xb) || !make_map(&mdl, dl_terms, 3, dl_dims, dl_str, db))
-      return cudaErrorInvalidValue;
-    uint32_t columns = 32;
-    while (columns < 2u * p.nu) columns *= 2;
-    const int smem = std::max(kTcMinSmem, p.w_stages * p.w_stage_bytes + 1024);
-    e = launch_pdl(router_wgrad_kernel, dim3(p.c_tiles * p.chunks), dim3(kTcThreads), smem, s, mx, mdl, part,
-                   static_cast<int64_t>(a.T), a.N, a.d, p.nu, p.n_boxes, p.c_tiles, p.chunk, p.w_stages, columns,
-                   a.status, a.timeout_ns);
+    const uint64_t xd[2] = {d, T}, xs[1] = {d * 2}, ld[3] = {np, T, 3}, ls[2] = {np * 2, T * np * 2};
+    const uint32_t xb[2] = {64, kKb}, lb[3] = {64, kKb, 1};
+    if (!make_map(&mx, a.x, 2, xd, xs, xb) || !make_map(&mdl, dl_terms, 3, ld, ls, lb)) return cudaErrorInvalidValue;
+    e = p.nu == 16   ? launch_wgrad<16>(mx, mdl, part, a, p, s)
+        : p.nu == 32 ? launch_wgrad<32>(mx, mdl, part, a, p, s)
+        : p.nu == 64 ? launch_wgrad<64>(mx, mdl, part, a, p, s)
+                     : launch_wgrad<128>(mx, mdl, part, a, p, s);
     if (e != cudaSuccess) return e;
   }
-  if (a.d_x != nullptr) {
+  if (want_x) {
     CUtensorMap mw, mdl;
-    const uint64_t wd[3] = {d, static_cast<uint64_t>(a.N), 3}, wst[2] = {d * 2, static_cast<uint64_t>(a.N) * d * 2};
-    const uint32_t wb[3] = {64, kKb, 1}, db[3] = {kKb, kXTileT, 1};
+    const uint64_t wd[3] = {d, static_cast<uint64_t>(a.N), 2}, wst[2] = {d * 2, static_cast<uint64_t>(a.N) * d * 2};
+    const uint64_t ld[3] = {np, T, 2}, ls[2] = {np * 2, T * np * 2};
+    const uint32_t wb[3] = {64, kKb, 1}, lb[3] = {kKb, kXTileT, 1};
+    // 16-bit elements either way: the copy does not look at the format
     if (!make_map(&mw, w_terms, 3, wd, wst, wb) ||
-        !make_map(&mdl, dl_terms, 3, dl_dims, dl_str, db, CU_TENSOR_MAP_SWIZZLE_64B))
+        !make_map(&mdl, dl16, 3, ld, ls, lb, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
+    static PerDeviceOnce once;
+    e = once.run([] {
+      return cudaFuncSetAttribute(router_dgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kXSmem);
+    });
+    if (e != cudaSuccess) return e;
     const int c_tiles = (a.d + kXTileC - 1) / kXTileC;
     const int64_t tiles = c_tiles * ((static_cast<int64_t>(a.T) + kXTileT - 1) / kXTileT);
     const int grid = static_cast<int>(std::min<int64_t>(tiles, di.sm_count));
-    e = launch_pdl(router_dgrad_kernel, dim3(grid), dim3(kTcThreads), kXSmem, s, mw, mdl, a.d_x,
-                   static_cast<int64_t>(a.T), a.N, a.d, c_tiles, tiles, a.accumulate, a.status, a.timeout_ns);
+    e = launch_pdl(router_dgrad_kernel, dim3(grid), dim3(kTcThreads), kXSmem, s, mw, mdl,
+                   static_cast<const int32_t*>(row_exp), a.d_x, static_cast<int64_t>(a.T), a.N, a.d, c_tiles, tiles,
+                   a.accumulate, a.status, a.timeout_ns);
     if (e != cudaSuccess) return e;
   }
-  if (a.d_w_router == nullptr && a.d_logit_bias == nullptr) return cudaSuccess;
-  const int64_t items = std::max<int64_t>(static_cast<int64_t>(a.N) * a.d / 4, a.N);
-  return launch_pdl(router_backward_sum_kernel, dim3(static_cast<unsigned>((items + 255) / 256)), dim3(256), 0, s,
-                    static_cast<const float*>(part), static_cast<const float*>(bias_part), a.d_w_router,
-                    a.d_logit_bias, p.chunks, p.split_ctas, a.N, a.d, a.accumulate);
+  if (!want_w && !want_b) return cudaSuccess;
+  return launch_sum(part, bias_part, a, p.chunks, p.split_ctas, s);
 }
 
 }  // namespace
 
 size_t router_backward_scratch_bytes(int64_t T, int N, int d) {
-  if (use_tensor_cores(T, N, d)) {
-    const TcPlan t = make_tc_plan(T, N, d);
-    return t.dl_bytes + t.w_bytes + t.part_bytes + t.bias_bytes;
-  }
+  if (use_tensor_cores(T, N, d)) return make_tc_plan(T, N, d).total();
   const Plan p = make_plan(T, N, d);
   return p.chunks > 1 ? static_cast<size_t>(p.chunks) * N * (d + 1) * sizeof(float) : 0;
 }
@@ -725,11 +893,7 @@ cudaError_t launch_router_backward(const RouterBackwardArgs& a, cudaStream_t s) 
   cudaError_t e = launch_pdl(router_backward_kernel, dim3(static_cast<unsigned>(p.w_ctas + x_ctas)),
                              dim3(kThreads), 0, s, p);
   if (e != cudaSuccess || !want_w || pl.chunks == 1) return e;
-  const int64_t items = std::max<int64_t>(static_cast<int64_t>(a.N) * a.d / 4, a.N);
-  return launch_pdl(router_backward_sum_kernel, dim3(static_cast<unsigned>((items + 255) / 256)),
-                    dim3(256), 0, s, static_cast<const float*>(p.part_w),
-                    static_cast<const float*>(p.part_b), a.d_w_router, a.d_logit_bias, pl.chunks, pl.chunks,
-                    a.N, a.d, a.accumulate);
+  return launch_sum(p.part_w, p.part_b, a, pl.chunks, pl.chunks, s);
 }
 
 }  // namespace moe
