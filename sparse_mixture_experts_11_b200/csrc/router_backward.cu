@@ -241,9 +241,6 @@ cudaError_t launch_sum(const float* part_w, const float* part_b, const RouterBac
 // step of 16 products. dx has 3 N / 16 <= 48 steps. dW's chains would be thousands; they are cut
 // after 48 steps (kFlush stages) and summed in fp32 registers by the epilogue warps, while the
 // other half of TMEM takes the next chain.
-// Both GEMMs put the axis d on the 128 rows of the MMA: the accumulator's lanes then run along
-// the contiguous axis of the outputs, and a warp's 32 lanes store 128 consecutive bytes straight
-// from registers.
 constexpr int kKb = 32;             // reduction elements of a stage
 constexpr int kBox = 64 * kKb * 2;  // one TMA box of an MN-major operand: 64 MN x 32 k, 128B-swizzled
 constexpr int kTcThreads = 320;     // TMA producer, MMA issuer, eight epilogue warps
@@ -251,7 +248,7 @@ constexpr int kTcMinSmem = 120 * 1024;  // one CTA an SM: the TMEM is not shared
 constexpr int kTcMaxSmem = 226 * 1024;  // dynamic; barriers beside it
 constexpr int kWTile = 256;         // columns of d a CTA of the weight gradient owns (two MMA row blocks)
 constexpr int kFlush = 8;           // stages of a chain: 8 * 2 steps * 3 terms = 48
-constexpr int kXTileC = 128, kXTileT = 256;
+constexpr int kXTileT = 128, kXTileC = 256;
 
 // Shared-memory descriptor of an MN-major operand of kKb k rows: groups of 8 k rows are 1024 bytes
 // (stride offset), blocks of 64 MN elements one box (leading offset).
@@ -477,7 +474,8 @@ __device__ __forceinline__ void tc_setup(TcShared& sh, int warp, uint32_t column
   tc_fence_after_sync();
 }
 
-// Weight gradient: one CTA for 256 columns of d, NU experts and one range of the tokens. A: x [t][c],
+// Weight gradient (the axis d on the MMA's rows: a warp's 32 lanes store 128 consecutive bytes of
+// dW from registers): one CTA for 256 columns of d, NU experts and one range of the tokens. A: x [t][c],
 // MN-major, two row blocks of 128 columns; B: the terms of dL [t][n], MN-major. D[c][n]: two chains
 // in TMEM, buffer u at columns [2 NU u, 2 NU (u + 1)), row block m at + NU m. The range's sum goes to
 // part [range][N][d].
@@ -622,25 +620,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-// dx: persistent CTAs over tiles of 128 columns of d x 256 tokens. A: W_r's terms [n][c], MN-major;
-// B: dL's terms [t][n], K-major; three products a k step into D[c][t]; two accumulators, so one
-// tile's epilogue runs beside the next one's MMAs. Accumulating adds in the L2 (a reduction
-// without a return: one addition an element, so the order is fixed, and no SM waits for the old
-// values).
-constexpr int kXStages = 4;
-constexpr int kXStageBytes = 2 * 2 * kBox + 2 * kXTileT * kKb * 2;
-constexpr int kXSmem = kXStages * kXStageBytes + 1024;
+// dx: persistent CTAs over tiles of 128 tokens x 256 columns of d. A: dL's terms [t][n], K-major; B:
+// W_r's terms [n][c], MN-major; three products a k step into D[t][c]; two accumulators, so one
+// tile's epilogue runs beside the next one's MMAs. A lane holds a token, so scaling back is one
+// factor a lane; 32 x 32 blocks go through shared memory to TMA stores. Accumulating is the same
+// store as a reduction: the L2 adds (one addition an element, so the order is fixed) and no SM
+// waits for the old values. (Lanes along c, and 128-byte reductions from registers: 299 us at
+// T = 16384, N = 256, d = 7168, bound by the issue of the reductions.)
+constexpr int kXStages = 3;
+constexpr int kXStageBytes = 2 * kXTileT * kKb * 2 + 2 * (kXTileC / 64) * kBox;
+constexpr int kXStaging = 32 * 32 * 4;  // one block; two for each epilogue warp
+constexpr int kXSmem = kXStages * kXStageBytes + 16 * kXStaging + 1024;
 static_assert(kXSmem <= kTcMaxSmem, "shared memory");
+
+__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
+}
 
 __global__ void __launch_bounds__(kTcThreads, 1)
     router_dgrad_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_dl,
-                        const int32_t* __restrict__ row_exp, float* __restrict__ d_x, int64_t T, int N, int d,
-                        int c_tiles, int64_t tiles, int accumulate, int* status, uint64_t timeout_ns) {
+                        const __grid_constant__ CUtensorMap tm_out, const int32_t* __restrict__ row_exp, int64_t T,
+                        int N, int d, int c_tiles, int64_t tiles, int accumulate, int* status,
+                        uint64_t timeout_ns) {
   extern __shared__ __align__(1024) uint8_t dyn_smem[];
   __shared__ TcShared sh;
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(dyn_smem) + 1023u) & ~1023u;
+  constexpr int kABytes = kXTileT * kKb * 2, kBBytes = kXTileC / 64 * kBox;  // one term
   tc_setup(sh, warp, 512);
   pdl_wait();
   const uint32_t tmem = sh.tmem;
@@ -653,7 +663,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const int c0 = static_cast<int>(t % c_tiles) * kXTileC;
         const int r0 = static_cast<int>(t / c_tiles) * kXTileT;
-        const int a_boxes = min(2, (d - c0) / 64);
+        const int boxes = min(kXTileC / 64, (d - c0) / 64);  // d is a multiple of 64
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const int s = it % kXStages;
           if (!mbar_wait(smem_u32(&sh.empty[s]), ((it / kXStages) & 1) ^ 1u, timeout_ns, &sh.abort)) {
@@ -661,12 +671,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             break;
           }
           const uint32_t fb = smem_u32(&sh.full[s]);
-          const uint32_t a = base + s * kXStageBytes, b = a + 2 * 2 * kBox;
-          mbar_arrive_expect_tx(fb, 2 * (a_boxes * kBox + kXTileT * kKb * 2));
+          const uint32_t a = base + s * kXStageBytes, b = a + 2 * kABytes;
+          mbar_arrive_expect_tx(fb, 2 * (kABytes + boxes * kBox));
           for (int k = 0; k < 2; ++k) {
-            for (int i = 0; i < a_boxes; ++i)
-              tma_load_3d(a + (2 * k + i) * kBox, &tm_w, fb, c0 + 64 * i, kb * kKb, k, last);
-            tma_load_3d(b + k * (kXTileT * kKb * 2), &tm_dl, fb, kb * kKb, r0, k, last);
+            tma_load_3d(a + k * kABytes, &tm_dl, fb, kb * kKb, r0, k, last);
+            for (int i = 0; i < boxes; ++i)
+              tma_load_3d(b + k * kBBytes + i * kBox, &tm_w, fb, c0 + 64 * i, kb * kKb, k, last);
           }
         }
       }
@@ -678,9 +688,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_wait(smem_u32(&sh.full[i % kXStages]), (i / kXStages) & 1, kDrainTimeoutNs, nullptr);
     }
   } else if (warp == 1) {
-    // fp16 operands (formats 0), A MN-major, B K-major
-    constexpr uint32_t idesc = (1u << 4) | (1u << 15) | (static_cast<uint32_t>(kXTileT >> 3) << 17) |
-                               (static_cast<uint32_t>(kXTileC >> 4) << 24);
+    // fp16 operands (formats 0), A K-major, B MN-major
+    constexpr uint32_t idesc = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(kXTileC >> 3) << 17) |
+                               (static_cast<uint32_t>(kXTileT >> 4) << 24);
     bool ok = true, issued = false;
     int it = 0, uc = 0;
     for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++uc) {
@@ -700,13 +710,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         tc_fence_after_sync();
         if (lane == 0) {
-          const uint32_t a = base + s * kXStageBytes, b = a + 2 * 2 * kBox;
+          const uint32_t a = base + s * kXStageBytes, b = a + 2 * kABytes;
           const int steps = min(kKb / 16, (N - kb * kKb + 15) / 16);
           for (int kk = 0; kk < steps; ++kk)
 #pragma unroll
             for (int k = 0; k < 3; ++k)  // terms (0, 0), (0, 1), (1, 0)
-              tc_mma_f16(tmem + buf * kXTileT, desc_mn(a + (k == 2 ? 2 * kBox : 0) + kk * 2048),
-                         desc_k64(b + (k == 1 ? kXTileT * kKb * 2 : 0) + kk * 32), idesc, kb > 0 || kk > 0 || k > 0);
+              tc_mma_f16(tmem + buf * kXTileC, desc_k64(a + (k == 2 ? kABytes : 0) + kk * 32),
+                         desc_mn(b + (k == 1 ? kBBytes : 0) + kk * 2048), idesc, kb > 0 || kk > 0 || k > 0);
           tc_commit(smem_u32(&sh.empty[s]));
         }
         issued = true;
@@ -724,17 +734,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_wait(smem_u32(&sh.done), 0, kDrainTimeoutNs, nullptr);
     }
   } else {
-    const int q = warp & 3;            // TMEM lane quadrant: columns q * 32 .. of the tile
-    const int half = (warp - 2) >> 2;  // tokens [half * 128, half * 128 + 128) of the tile
-    int uc = 0;
+    const int q = warp & 3;            // TMEM lane quadrant: tokens q * 32 .. of the tile
+    const int half = (warp - 2) >> 2;  // columns [half * 128, half * 128 + 128) of the tile
+    const uint32_t stage0 = base + kXStages * kXStageBytes + (warp - 2) * 2 * kXStaging;
+    int uc = 0, n = 0;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++uc) {
       const int buf = uc & 1;
-      const int c = static_cast<int>(t % c_tiles) * kXTileC + q * 32;
-      const int64_t r0 = t / c_tiles * kXTileT + half * 128;
-      float scale[4];  // 2^(a_t) of tokens r0 + 32 j + lane
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        scale[j] = r0 + 32 * j + lane < T ? scalbnf(1.0f, max(-126, min(127, row_exp[r0 + 32 * j + lane]))) : 0.f;
+      const int64_t r0 = t / c_tiles * kXTileT + q * 32;
+      const int c0 = static_cast<int>(t % c_tiles) * kXTileC + half * 128;
+      const int e = r0 + lane < T ? row_exp[r0 + lane] : 0;
+      // 2^(a_t - 28) in two factors, the second 1 but for tokens below 2^-98
+      const float f = scalbnf(1.0f, min(127, max(-126, e - 28)));
+      const float f2 = scalbnf(1.0f, max(-149, min(0, e - 28 + 126)));
+      const bool tiny = __any_sync(kFull, f2 != 1.0f);
       const bool got = mbar_wait(smem_u32(&sh.tfull[buf]), (uc >> 1) & 1, timeout_ns, &sh.abort);
       if (!__all_sync(kFull, got)) {
         sh.abort = 1;
@@ -742,29 +754,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         break;
       }
       tc_fence_after_sync();
-      const uint32_t row = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * kXTileT + half * 128;
-      if (c < d) {
+      const uint32_t row = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * kXTileC + half * 128;
+#pragma unroll 1
+      for (int cc = 0; cc < 128 && c0 + cc < d && r0 < T; cc += 32, ++n) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(row + cc, v);
+        tmem_ld_wait();
+        const uint32_t stage = stage0 + (n & 1) * kXStaging;
+        uint8_t* const stg = dyn_smem + (stage - smem_u32(dyn_smem));
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the block before the last
+        __syncwarp();
+        float r[32];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (r0 + 32 * j >= T) break;  // warp-uniform
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(row + 32 * j, v);
-          tmem_ld_wait();
-          float* out = d_x + (r0 + 32 * j) * d + c + lane;
-          const int rows = static_cast<int>(min(static_cast<int64_t>(32), T - r0 - 32 * j));
+        for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(v[i]) * f;
+        if (tiny) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float r = __uint_as_float(v[i]) * 0x1p-28f * __shfl_sync(kFull, scale[j], i);
-            if (i < rows) {
-              if (accumulate) atomicAdd(out + static_cast<int64_t>(i) * d, r);
-              else __stcs(out + static_cast<int64_t>(i) * d, r);
-            }
-          }
+          for (int i = 0; i < 32; ++i) r[i] *= f2;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<float4*>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+              make_float4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+        fence_proxy_async_smem();  // generic stores -> visible to the TMA engine
+        __syncwarp();
+        if (lane == 0) {  // rows past T and columns past d are not written
+          if (accumulate) tma_reduce_add_2d(&tm_out, stage, c0 + cc, static_cast<int>(r0));
+          else tma_store_2d(&tm_out, stage, c0 + cc, static_cast<int>(r0));
+          tma_store_commit();
         }
       }
       tc_fence_before_sync();
       mbar_arrive(smem_u32(&sh.tempty[buf]));
     }
+    if (lane == 0) tma_store_wait_all();  // every store of this warp has landed
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -831,13 +853,16 @@ cudaError_t launch_tc(const RouterBackwardArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   if (want_x) {
-    CUtensorMap mw, mdl;
+    CUtensorMap mw, mdl, mo;
+    const uint64_t od[2] = {d, T}, os[1] = {d * 4};
+    const uint32_t ob[2] = {32, 32};
     const uint64_t wd[3] = {d, static_cast<uint64_t>(a.N), 2}, wst[2] = {d * 2, static_cast<uint64_t>(a.N) * d * 2};
     const uint64_t ld[3] = {np, T, 2}, ls[2] = {np * 2, T * np * 2};
     const uint32_t wb[3] = {64, kKb, 1}, lb[3] = {kKb, kXTileT, 1};
     // 16-bit elements either way: the copy does not look at the format
     if (!make_map(&mw, w_terms, 3, wd, wst, wb) ||
-        !make_map(&mdl, dl16, 3, ld, ls, lb, CU_TENSOR_MAP_SWIZZLE_64B))
+        !make_map(&mdl, dl16, 3, ld, ls, lb, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !make_map_f32(&mo, a.d_x, 2, od, os, ob))
       return cudaErrorInvalidValue;
     static PerDeviceOnce once;
     e = once.run([] {
@@ -847,8 +872,8 @@ cudaError_t launch_tc(const RouterBackwardArgs& a, cudaStream_t s) {
     const int c_tiles = (a.d + kXTileC - 1) / kXTileC;
     const int64_t tiles = c_tiles * ((static_cast<int64_t>(a.T) + kXTileT - 1) / kXTileT);
     const int grid = static_cast<int>(std::min<int64_t>(tiles, di.sm_count));
-    e = launch_pdl(router_dgrad_kernel, dim3(grid), dim3(kTcThreads), kXSmem, s, mw, mdl,
-                   static_cast<const int32_t*>(row_exp), a.d_x, static_cast<int64_t>(a.T), a.N, a.d, c_tiles, tiles,
+    e = launch_pdl(router_dgrad_kernel, dim3(grid), dim3(kTcThreads), kXSmem, s, mw, mdl, mo,
+                   static_cast<const int32_t*>(row_exp), static_cast<int64_t>(a.T), a.N, a.d, c_tiles, tiles,
                    a.accumulate, a.status, a.timeout_ns);
     if (e != cudaSuccess) return e;
   }
