@@ -143,13 +143,21 @@ def _check(status: int, where: str) -> None:
         raise MoeError(status, where)
 
 
-def _stream(stream) -> ctypes.c_void_p:
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object made
+
+
+def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None, allow_none=False):
+    if (t is not None and t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype)
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
     if t is None:
         if allow_none:
             return None
@@ -160,9 +168,7 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None, allow_non
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return ctypes.c_void_p(t.data_ptr())
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _nbytes(t: Optional[torch.Tensor]) -> int:
@@ -488,12 +494,12 @@ def backward_into(dims: Dims, x, w_router, w_gate_up, w_down, fwd_ws, d_out, d_x
 
 
 # ----------------------------------------------------------------------------- training
-def _one_device(**tensors) -> None:
+def _one_device(names: str, *tensors) -> None:
     """All tensors on the current device: the library launches there."""
     here = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.is_cuda and t.device.index != here:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+    for i, t in enumerate(tensors):
+        if t is not None and t.is_cuda and t.get_device() != here:
+            raise ValueError(f"{names.split()[i]} is on {t.device}, the current device is cuda:{here}")
 
 
 def balance_loss(dims: Dims, logits, topk_idx, token_mask, counts, n_tokens, prob_mean, loss,
@@ -503,9 +509,8 @@ def balance_loss(dims: Dims, logits, topk_idx, token_mask, counts, n_tokens, pro
     per-expert counts, and the gradient of the logits (d_logits may be None). loss [3] receives
     balance + z, balance, z; d_loss, a scalar tensor or None (1), is the total's gradient."""
     T, N, k = dims.T, dims.n_experts, dims.top_k
-    _one_device(logits=logits, topk_idx=topk_idx, token_mask=token_mask, counts=counts,
-                n_tokens=n_tokens, prob_mean=prob_mean, loss=loss, d_logits=d_logits, ws=ws,
-                d_loss=d_loss)
+    _one_device("logits topk_idx token_mask counts n_tokens prob_mean loss d_logits ws d_loss", logits,
+                topk_idx, token_mask, counts, n_tokens, prob_mean, loss, d_logits, ws, d_loss)
     _check(_lib.moe_balance_loss(
         ctypes.byref(dims), _ptr(logits, "logits", torch.float32, (T, N)),
         _ptr(topk_idx, "topk_idx", torch.int32, (T, k)),
@@ -534,8 +539,8 @@ def router_backward(dims: Dims, x, w_router, d_logits, d_x, d_w_router, d_logit_
     """Gradient of the linear router for a dense gradient of the logits; outputs (each may be
     None) are written, or added to with accumulate (after backward_into)."""
     T, d, N = dims.T, dims.d_model, dims.n_experts
-    _one_device(x=x, w_router=w_router, d_logits=d_logits, d_x=d_x, d_w_router=d_w_router,
-                d_logit_bias=d_logit_bias, ws=ws)
+    _one_device("x w_router d_logits d_x d_w_router d_logit_bias ws", x, w_router, d_logits, d_x,
+                d_w_router, d_logit_bias, ws)
     _check(_lib.moe_router_backward(
         ctypes.byref(dims), _ptr(x, "x", torch.bfloat16, (T, d)),
         _ptr(w_router, "w_router", torch.float32, (N, d)),
@@ -586,7 +591,7 @@ def grad_norm(plan: _Plan, max_norm: float, norm, scale, ws, stream=None) -> Non
     """norm [1]: the global norm of the plan's gradients; scale [1]: min(1, max_norm / (norm +
     1e-6)), or NaN (adamw_step then leaves the step out) where the norm is not finite."""
     plan.check_device()
-    _one_device(norm=norm, scale=scale, ws=ws)
+    _one_device("norm scale ws", norm, scale, ws)
     if plan.array._type_ is not GradTensor:
         raise ValueError("grad_norm takes a plan of grad_plan()")
     _check(_lib.moe_grad_norm(plan.array, plan.n, float(max_norm), _ptr(norm, "norm", torch.float32, (1,)),
@@ -654,10 +659,9 @@ def adamw_step(plan: _Plan, step, *, lr=1e-3, betas=(0.9, 0.999), eps: float = 1
         raise ValueError("adamw_step takes a plan of adamw_plan()")
     step_t = step if isinstance(step, torch.Tensor) else None
     lr_t = lr if isinstance(lr, torch.Tensor) else None
-    _one_device(step=step_t, lr=lr_t, grad_scale=grad_scale)
-    cfg = AdamWConfig(0.0 if lr_t is not None else float(lr), float(betas[0]), float(betas[1]), float(eps),
-                      1 if step_t is not None else int(step), int(seed) & 0xFFFFFFFF,
-                      _ptr(step_t, "step", torch.int32, (1,), allow_none=True),
+    _one_device("step lr grad_scale", step_t, lr_t, grad_scale)
+    cfg = AdamWConfig(0.0 if lr_t is not None else lr, betas[0], betas[1], eps, 1 if step_t is not None else step,
+                      seed & 0xFFFFFFFF, _ptr(step_t, "step", torch.int32, (1,), allow_none=True),
                       _ptr(lr_t, "lr", torch.float32, (1,), allow_none=True),
                       _ptr(grad_scale, "grad_scale", torch.float32, (1,), allow_none=True))
     _check(_lib.moe_adamw_step(plan.array, plan.n, ctypes.byref(cfg), _stream(stream)), "moe_adamw_step")

@@ -70,22 +70,24 @@ struct NormEntry {
   int32_t chunk0;
   int32_t bf16;
 };
-constexpr int kNormTable = 1024;  // entries of one launch: 24 KB of kernel parameters
+// Entries of one launch: 24 KB of kernel parameters, or 0.8 KB for short lists (the launch copies
+// its parameters: 1.5 us more for the large table).
+constexpr int kNormTable = 1024, kNormTableShort = 32;
+template <int CAP>
 struct NormTable {
   int n, chunks, chunk;  // chunk: elements of a chunk
   int first, last;       // first launch of the call: slots start at zero; last: it finishes
-  NormEntry e[kNormTable];
+  NormEntry e[CAP];
 };
 
 // Sum of squares. A thread adds 8 squares in fp32 and the eights in fp64 (fp32 alone would lose
 // the small terms of a sum of 1e9); warps, CTAs and the CTAs' slots add in a fixed order. The
 // last CTA to arrive adds the slots and forms the norm and the clipping scale.
-__global__ void __launch_bounds__(kOptThreads) grad_norm_kernel(const __grid_constant__ NormTable tab,
-                                                                double* __restrict__ slots,
-                                                                int* __restrict__ counter,
-                                                                float max_norm,
-                                                                float* __restrict__ norm,
-                                                                float* __restrict__ scale) {
+template <int CAP>
+__global__ void __launch_bounds__(kOptThreads)
+    grad_norm_kernel(const __grid_constant__ NormTable<CAP> tab, double* __restrict__ slots,
+                     int* __restrict__ counter, float max_norm, float* __restrict__ norm,
+                     float* __restrict__ scale) {
   __shared__ double s_sum[kOptWarps];
   __shared__ int s_last;
   pdl_trigger();
@@ -545,15 +547,15 @@ __global__ void __launch_bounds__(kOptThreads, BITS8 ? 4 : 3)
   }
 }
 
-constexpr int kAdamTable = 384;  // entries of one launch: 30 KB of kernel parameters
+// entries of one launch: 30 KB of kernel parameters, or 2.5 KB for short lists
+constexpr int kAdamTable = 384, kAdamTableShort = 32;
 static_assert(sizeof(AdamTable<kAdamTable>) + sizeof(AdamScalars) <= 32764, "kernel parameters");
-static_assert(sizeof(NormTable) + 64 <= 32764, "kernel parameters");
+static_assert(sizeof(NormTable<kNormTable>) + 64 <= 32764, "kernel parameters");
 
-// The tensors of one kind (8-bit or fp32 moments) of the list, kAdamTable a launch.
-template <bool BITS8>
+// The tensors of one kind (8-bit or fp32 moments) of the list, CAP a launch.
+template <bool BITS8, int CAP>
 cudaError_t launch_adamw_kind(const moe_adamw_tensor* tensors, int n, const AdamScalars& sc, int sms,
                               cudaStream_t s) {
-  auto kern = adamw_kernel<BITS8, kAdamTable>;
   int64_t total = 0;  // tiles
   for (int i = 0; i < n; ++i)
     if (tensors[i].numel > 0 && (tensors[i].state_bits == 8) == BITS8)
@@ -567,12 +569,12 @@ cudaError_t launch_adamw_kind(const moe_adamw_tensor* tensors, int n, const Adam
   const int64_t resident = static_cast<int64_t>(sms) * 4;
   int chunk_tiles = 1;
   while (BITS8 && chunk_tiles < 32 && total / chunk_tiles > 8 * resident) chunk_tiles *= 2;
-  AdamTable<kAdamTable> tab;
+  AdamTable<CAP> tab;
   for (int i = 0; i < n;) {
     tab.n = 0;
     tab.chunk_tiles = chunk_tiles;
     int64_t chunks = 0;
-    for (; i < n && tab.n < kAdamTable; ++i) {
+    for (; i < n && tab.n < CAP; ++i) {
       const moe_adamw_tensor& in = tensors[i];
       if (in.numel == 0 || (in.state_bits == 8) != BITS8) continue;
       const int64_t c = ((in.numel - 1) / (kTileBlocks * kQBlock) + chunk_tiles) / chunk_tiles;
@@ -596,36 +598,33 @@ cudaError_t launch_adamw_kind(const moe_adamw_tensor* tensors, int n, const Adam
     if (chunks == 0) break;
     tab.chunks = static_cast<int>(chunks);
     const int grid = static_cast<int>(BITS8 ? std::min<int64_t>(chunks, resident) : chunks);
-    const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kOptThreads), 0, s, tab, sc);
+    const cudaError_t e = launch_pdl(adamw_kernel<BITS8, CAP>, dim3(grid), dim3(kOptThreads), 0, s, tab, sc);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
-}  // namespace
-
-cudaError_t launch_grad_norm(const moe_grad_tensor* tensors, int n, float max_norm, float* norm,
-                             float* scale, void* ws, cudaStream_t s) {
-  DeviceInfo di;
-  cudaError_t e = device_info(&di);
-  if (e != cudaSuccess) return e;
+template <int CAP>
+cudaError_t launch_grad_norm_tables(const moe_grad_tensor* tensors, int n, float max_norm, float* norm,
+                                    float* scale, void* ws, int sms, cudaStream_t s) {
   int* counter = reinterpret_cast<int*>(static_cast<char*>(ws) + 64);
   double* slots = reinterpret_cast<double*>(static_cast<char*>(ws) + kStatusBytes);
   int64_t total = 0;
   for (int i = 0; i < n; ++i) total += tensors[i].numel;
-  const int grid = std::min(kGradNormSlots, di.sm_count * 6);
   // chunks: small enough that a small total reaches every SM, large enough (32 KB of bf16) that
-  // finding the tensor costs nothing beside it
+  // finding the tensor costs nothing beside it; no more CTAs than 2048-element chunks
+  const int most = std::min(kGradNormSlots, sms * 6);
   int chunk = 2048;
-  while (chunk < 16384 && total / chunk > grid) chunk *= 2;
-  NormTable tab;
+  while (chunk < 16384 && total / chunk > most) chunk *= 2;
+  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, total / chunk + n)));
+  NormTable<CAP> tab;
   tab.first = 1;
   int i = 0;
   do {
     tab.n = 0;
     tab.chunk = chunk;
     int64_t chunks = 0;
-    for (; i < n && tab.n < kNormTable; ++i) {
+    for (; i < n && tab.n < CAP; ++i) {
       if (tensors[i].numel == 0) continue;
       const int64_t c = (tensors[i].numel + chunk - 1) / chunk;
       if (chunks + c > INT32_MAX) return cudaErrorInvalidValue;
@@ -638,12 +637,24 @@ cudaError_t launch_grad_norm(const moe_grad_tensor* tensors, int n, float max_no
     }
     tab.chunks = static_cast<int>(chunks);
     tab.last = i >= n;
-    e = launch_pdl(grad_norm_kernel, dim3(grid), dim3(kOptThreads), 0, s, tab, slots, counter,
-                   max_norm, norm, scale);
+    const cudaError_t e = launch_pdl(grad_norm_kernel<CAP>, dim3(grid), dim3(kOptThreads), 0, s, tab, slots,
+                                     counter, max_norm, norm, scale);
     if (e != cudaSuccess) return e;
     tab.first = 0;
   } while (i < n);
   return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_grad_norm(const moe_grad_tensor* tensors, int n, float max_norm, float* norm,
+                             float* scale, void* ws, cudaStream_t s) {
+  DeviceInfo di;
+  const cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  return n <= kNormTableShort
+             ? launch_grad_norm_tables<kNormTableShort>(tensors, n, max_norm, norm, scale, ws, di.sm_count, s)
+             : launch_grad_norm_tables<kNormTable>(tensors, n, max_norm, norm, scale, ws, di.sm_count, s);
 }
 
 cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int n, const moe_adamw_config& cfg,
@@ -670,8 +681,12 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int n, const moe_adamw
   sc.step_dev = cfg.step_dev;
   sc.lr_dev = cfg.lr_dev;
   sc.grad_scale = cfg.grad_scale;
-  e = launch_adamw_kind<false>(tensors, n, sc, di.sm_count, s);
-  return e != cudaSuccess ? e : launch_adamw_kind<true>(tensors, n, sc, di.sm_count, s);
+  if (n <= kAdamTableShort) {
+    e = launch_adamw_kind<false, kAdamTableShort>(tensors, n, sc, di.sm_count, s);
+    return e != cudaSuccess ? e : launch_adamw_kind<true, kAdamTableShort>(tensors, n, sc, di.sm_count, s);
+  }
+  e = launch_adamw_kind<false, kAdamTable>(tensors, n, sc, di.sm_count, s);
+  return e != cudaSuccess ? e : launch_adamw_kind<true, kAdamTable>(tensors, n, sc, di.sm_count, s);
 }
 
 }  // namespace moe
