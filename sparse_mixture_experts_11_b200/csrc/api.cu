@@ -126,7 +126,7 @@ size_t shared_region_bytes(const moe_dims* d) {
   const size_t ffn = round_up(ffn_plan(d).part_bytes, 256);
   const size_t stats = round_up(moe::router_stats_scratch_bytes(d->T, d->n_experts), 256);
   const size_t redirect = round_up(moe::redirect_scratch_bytes(d->T, d->top_k), 256);
-  const size_t balance = round_up(moe::balance_scratch_bytes(d->T, d->n_experts, d->top_k), 256);
+  const size_t balance = round_up(moe::balance_scratch_bytes(d->T, d->n_experts), 256);
   return std::max({routing, ffn, stats, redirect, balance});
 }
 

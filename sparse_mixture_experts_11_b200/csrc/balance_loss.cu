@@ -10,7 +10,7 @@
 // from topk_idx alone (4 k bytes a token against 4 N), and every CTA holds them while it reads
 // its tokens' logits once and writes their gradients.
 //
-//   pass 1 (only past kInlinePairs pairs)  per-chunk counts, one row of the workspace a chunk
+//   pass 1 (only past kInlineTokens tokens)  per-chunk counts, one row of the workspace a chunk
 //   pass 2  the counts (of the rows, or of topk_idx itself), then the tokens; P's partial sums
 //           leave one row a CTA, and the last CTA to finish adds the rows in order
 // No floating-point atomics: the results do not depend on the order the CTAs run in.
@@ -28,18 +28,21 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBalThreads = 512;
 constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kBalPerSm = 1;
 constexpr int kMaxN = 256;
-// Up to here every CTA counts all pairs itself; past it the pairs are counted in chunks first.
-constexpr int64_t kInlinePairs = 4096;
+// Up to here every CTA counts all tokens' pairs itself (two rounds of its threads); past it they are
+// counted in chunks by a first launch. Device time of both, us: T = 1000, N = 64, k = 4 6.4 and
+// 7.7; T = 2048, k = 4 8.0 and 8.6; T = 4096, k = 1 11.0 and 9.9; k = 4 11.5 and 10.3.
+constexpr int64_t kInlineTokens = 2048;
 constexpr int kCountRows = 64;  // rows of partial counts, at most
 
 struct CountPlan {
   int64_t chunk;  // tokens a row
   int rows;       // 0: counted inline
 };
-CountPlan count_plan(int64_t T, int64_t k) {
-  if (T * k <= kInlinePairs) return {0, 0};
-  const int64_t want = std::min<int64_t>(kCountRows, (T * k + kInlinePairs - 1) / kInlinePairs);
+CountPlan count_plan(int64_t T) {
+  if (T <= kInlineTokens) return {0, 0};
+  const int64_t want = std::min<int64_t>(kCountRows, (T + kBalThreads - 1) / kBalThreads);
   const int64_t chunk = (T + want - 1) / want;
   return {chunk, static_cast<int>((T + chunk - 1) / chunk)};
 }
@@ -58,28 +61,38 @@ TokenShape token_shape(int N) {
 }
 
 // CTAs of pass 2: one an SM, fewer when the tokens do not fill them.
-int balance_ctas(int T, int N, int sms) {
+int balance_ctas(int T, int N, int most) {
   const int per_cta = kBalWarps * (32 / token_shape(N).g);
-  return std::max(1, std::min((T + per_cta - 1) / per_cta, sms));
+  return std::max(1, std::min((T + per_cta - 1) / per_cta, most));
 }
 // floats of a CTA's row: N probabilities rounded up to four, then sum of lse^2 and padding
 __host__ __device__ constexpr int row_floats(int N) { return (N + 3) / 4 * 4 + 4; }
 
 // Counts of tokens [t0, t1): pairs of counted tokens that chose expert e into s_cnt[e], counted
-// tokens into s_cnt[N]. Integer shared-memory atomics: the result has no order.
+// tokens into s_cnt[N]. A thread takes two tokens a round, their loads issued together. Integer
+// shared-memory atomics: the result has no order, and a token's choices differ, so at most 32 / k
+// lanes of an access meet at one expert.
 __device__ __forceinline__ void count_pairs(const int32_t* __restrict__ topk_idx,
                                             const uint8_t* __restrict__ mask, int64_t t0, int64_t t1,
                                             int N, int k, int* s_cnt) {
-  const int64_t q1 = t1 * k;
-  for (int64_t q = t0 * k + threadIdx.x; q < q1; q += kBalThreads) {
-    const int e = topk_idx[q];
-    if (e >= 0 && e < N && (mask == nullptr || mask[q / k] != 0)) atomicAdd(&s_cnt[e], 1);
-  }
   int n = 0;
-  if (mask == nullptr) {
-    if (threadIdx.x == 0) n = static_cast<int>(t1 - t0);
-  } else {
-    for (int64_t t = t0 + threadIdx.x; t < t1; t += kBalThreads) n += mask[t] != 0;
+  for (int64_t t = t0 + threadIdx.x; t < t1; t += 2 * kBalThreads) {
+    int e[2][8];
+    bool keep[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t r = t + u * kBalThreads;
+      keep[u] = r < t1 && (mask == nullptr || mask[r] != 0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[u][j] = r < t1 && j < k ? __ldg(topk_idx + r * k + j) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      n += keep[u];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (keep[u] && e[u][j] >= 0 && e[u][j] < N) atomicAdd(&s_cnt[e[u][j]], 1);
+    }
   }
   n = __reduce_add_sync(kFull, n);
   if ((threadIdx.x & 31) == 0 && n != 0) atomicAdd(&s_cnt[N], n);
@@ -118,7 +131,7 @@ struct BalanceParams {
 };
 
 template <int G, int C, int VEC>
-__global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const BalanceParams a) {
+__global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(const BalanceParams a) {
   constexpr int V = C * VEC;          // values a lane holds of a token
   constexpr int kGroups = 32 / G;     // tokens a warp takes at once
   __shared__ int s_cnt[kMaxN + 1];
@@ -131,14 +144,40 @@ __global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const Balance
   for (int e = threadIdx.x; e <= N; e += kBalThreads) s_cnt[e] = 0;
   pdl_trigger();
   pdl_wait();
+  const int gl = lane % G;  // lane within the token's group
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kBalWarps * kGroups;
+  int64_t t = (blockIdx.x * kBalWarps + warp) * kGroups + lane / G;
+  // a token's logits, -inf where there is none (past N, past T, or padding: not even read)
+  auto load = [&](int64_t tok, float (&x)[V]) {
+    const bool counted = tok < a.T && (a.mask == nullptr || a.mask[tok] != 0);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int e = (c * G + gl) * VEC;
+      if (VEC == 4) {
+        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (counted && e < N) q = __ldcs(reinterpret_cast<const float4*>(a.logits + tok * N + e));
+        x[c * VEC] = q.x;
+        x[c * VEC + VEC / 4] = q.y;
+        x[c * VEC + VEC / 2] = q.z;
+        x[c * VEC + VEC * 3 / 4] = q.w;
+      } else {
+        x[c] = counted && e < N ? __ldcs(a.logits + tok * N + e) : -INFINITY;
+      }
+    }
+  };
+  float next[V];
+  load(t, next);  // under way while the counts are formed
   __syncthreads();
   if (a.n_count_rows == 0) {
     count_pairs(a.topk_idx, a.mask, 0, a.T, N, a.k, s_cnt);
   } else {
-    const int items = a.n_count_rows * (N + 1);
-    for (int i = threadIdx.x; i < items; i += kBalThreads) {
-      const int c = __ldcg(a.count_rows + i);
-      if (c != 0) atomicAdd(&s_cnt[i % (N + 1)], c);
+    // threads of a column take every (kBalThreads / columns)-th row
+    const int cols = N + 1, groups = max(1, kBalThreads / cols);
+    for (int i = threadIdx.x; i < cols * groups; i += kBalThreads) {
+      int sum = 0;
+#pragma unroll 8
+      for (int r = i / cols; r < a.n_count_rows; r += groups) sum += __ldcg(a.count_rows + r * cols + i % cols);
+      if (sum != 0) atomicAdd(&s_cnt[i % cols], sum);
     }
   }
   __syncthreads();
@@ -151,7 +190,6 @@ __global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const Balance
   const float g = a.d_loss != nullptr ? *a.d_loss : 1.0f;
   const float c_bal = g * a.alpha * static_cast<float>(N) * inv_n;
   const float c_z = g * 2.0f * a.z_coef * inv_n;
-  const int gl = lane % G;  // lane within the token's group
   float f[V], acc[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -160,29 +198,15 @@ __global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const Balance
     acc[j] = 0.f;
   }
   float z_acc = 0.f;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kBalWarps * kGroups;
-  for (int64_t t = (blockIdx.x * kBalWarps + warp) * kGroups + lane / G; t - lane / G < a.T; t += stride) {
-    const bool have = t < a.T;
-    const bool counted = have && (a.mask == nullptr || a.mask[t] != 0);
-    const int64_t row = t * N;
+  for (; t - lane / G < a.T; t += stride) {
     float v[V];
     float m = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int e = (c * G + gl) * VEC;
-      if (VEC == 4) {
-        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (counted && e < N) q = __ldg(reinterpret_cast<const float4*>(a.logits + row + e));
-        v[c * VEC] = q.x;
-        v[c * VEC + VEC / 4] = q.y;
-        v[c * VEC + VEC / 2] = q.z;
-        v[c * VEC + VEC * 3 / 4] = q.w;
-      } else {
-        v[c] = counted && e < N ? __ldg(a.logits + row + e) : -INFINITY;
-      }
+    for (int j = 0; j < V; ++j) {
+      v[j] = next[j];
+      m = fmaxf(m, v[j]);
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) m = fmaxf(m, v[j]);
+    load(t + stride, next);
 #pragma unroll
     for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
     const float base = m == -INFINITY ? 0.f : m;  // a row of -inf only (or one that is not counted)
@@ -207,7 +231,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const Balance
       acc[j] += v[j];
     }
     if (gl == 0) z_acc += lse * lse;
-    if (a.d_logits != nullptr && have) {
+    if (a.d_logits != nullptr && t < a.T) {
 #pragma unroll
       for (int j = 0; j < V; ++j) v[j] *= c_bal * (f[j] - inner) + c_z * lse;
 #pragma unroll
@@ -215,10 +239,10 @@ __global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const Balance
         const int e = (c * G + gl) * VEC;
         if (e < N) {
           if (VEC == 4)
-            *reinterpret_cast<float4*>(a.d_logits + row + e) =
+            *reinterpret_cast<float4*>(a.d_logits + t * N + e) =
                 make_float4(v[c * VEC], v[c * VEC + VEC / 4], v[c * VEC + VEC / 2], v[c * VEC + VEC * 3 / 4]);
           else
-            a.d_logits[row + e] = v[c];
+            a.d_logits[t * N + e] = v[c];
         }
       }
     }
@@ -324,9 +348,9 @@ __global__ void __launch_bounds__(kBalThreads) balance_loss_kernel(const Balance
 
 }  // namespace
 
-size_t balance_scratch_bytes(int64_t T, int N, int k) {
+size_t balance_scratch_bytes(int64_t T, int N) {
   if (T == 0) return 0;
-  const size_t rows = static_cast<size_t>(count_plan(T, k).rows) * (N + 1) * sizeof(int32_t);
+  const size_t rows = static_cast<size_t>(count_plan(T).rows) * (N + 1) * sizeof(int32_t);
   return (rows + 15) / 16 * 16 +
          static_cast<size_t>(balance_ctas(static_cast<int>(T), N, kBalanceMaxCtas)) * row_floats(N) *
              sizeof(float);
@@ -336,7 +360,7 @@ cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
-  const CountPlan cp = count_plan(a.T, a.k);
+  const CountPlan cp = count_plan(a.T);
   BalanceParams p{};
   p.logits = a.logits;
   p.topk_idx = a.topk_idx;
@@ -372,7 +396,7 @@ cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
     kern = ts.g == 8 ? balance_loss_kernel<8, 1, 1> : ts.g == 16 ? balance_loss_kernel<16, 1, 1>
          : ts.c == 1 ? balance_loss_kernel<32, 1, 1> : ts.c == 2 ? balance_loss_kernel<32, 2, 1>
          : ts.c == 4 ? balance_loss_kernel<32, 4, 1> : balance_loss_kernel<32, 8, 1>;
-  const int grid = balance_ctas(a.T, a.N, std::min(di.sm_count, kBalanceMaxCtas));
+  const int grid = balance_ctas(a.T, a.N, std::min(di.sm_count * kBalPerSm, kBalanceMaxCtas));
   return launch_pdl(kern, dim3(grid), dim3(kBalThreads), 0, s, p);
 }
 

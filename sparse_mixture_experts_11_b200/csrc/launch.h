@@ -320,7 +320,7 @@ struct BalanceArgs {
   int* counter;
   int T, N, k;
 };
-size_t balance_scratch_bytes(int64_t T, int N, int k);
+size_t balance_scratch_bytes(int64_t T, int N);
 cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s);
 
 // Gradient of the linear router for a dense gradient of the logits (router_backward.cu). Null

@@ -21,7 +21,6 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256;
-constexpr double kTcWork = 33554432.0;
 constexpr int kWExperts = 16, kWCols = 128, kWTokens = 32;
 constexpr int kXTokens = 16, kXCols = 256, kXExperts = 64;
 
@@ -796,8 +795,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-// Tensor cores where the products are worth the five launches.
-bool use_tensor_cores(int64_t T, int N, int d) { return T >= 256 && static_cast<double>(T) * N * d >= kTcWork; }
+// Tensor cores where the products are worth the five launches, from T N d = 2^26 on. Device time
+// of the two paths, CUDA cores first, us, at (T, d, N): (256, 1024, 64) 12.0, 20.7; (512, 2880, 32) 19.1,
+// 20.7; (1024, 1024, 64) 20.1, 21.7; (64, 4096, 256) 37.0, 30.7; (4096, 512, 64) 36.6, 23.9;
+// (4096, 2880, 32) 94, 33; (1024, 4096, 128) 126, 29. Below 64 tokens a row block of the MMA is half empty.
+bool use_tensor_cores(int64_t T, int N, int d) { return T >= 64 && static_cast<double>(T) * N * d >= 67108864.0; }
 
 template <int NU>
 cudaError_t launch_wgrad(const CUtensorMap& mx, const CUtensorMap& mdl, float* part, const RouterBackwardArgs& a,
