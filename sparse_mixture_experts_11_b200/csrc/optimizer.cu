@@ -22,6 +22,11 @@
 // probability of the part cut off keeps its expectation. A nonzero r keeps a nonzero code, so
 // that no m is divided by eps alone. The random bits are a function of (seed, step, place of the
 // tensor in the list, element), so a step is reproducible.
+// Where a value lies next to a border of the codes, its last bit decides between codes 6 to 12 %
+// apart, and a block's next scale can hang on one code. So with 8 bits m', v' and sqrt(v'), and the
+// update of a bf16 parameter without a master copy, are computed in the order of the
+// formulas, every operation rounded by itself (no fused multiply-add; square root, quotient and
+// reciprocal to nearest): any fp32 implementation of these lines has the same results, bit by bit.
 // A bf16 parameter without an fp32 master copy is rounded the same way: most updates are below
 // half its spacing.
 #include <math.h>
@@ -188,9 +193,9 @@ struct AdamEntry {
   uint8_t params, grad_bf16;
 };
 struct AdamScalars {
-  float lr, b1, omb1, b2, root_b2, root_omb2, eps;  // omb: 1 - beta; root: square roots
-  float inv_bc1, inv_sqrt_bc2;  // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
-  double beta1, beta2;          // for a step number read on the device
+  float b1, omb1, b2, omb2, eps;  // omb: 1 - beta
+  float step_size, inv_sqrt_bc2;  // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+  double rate, beta1, beta2;      // for a step number or rate read on the device
   uint32_t seed;
   int32_t step;
   const int32_t* step_dev;
@@ -203,13 +208,12 @@ struct AdamTable {
   AdamEntry e[CAP];
 };
 
-struct StepScalars {  // what every element needs
-  float lr_wd1, neg_step, b1, b2;  // 1 - lr wd, -lr / (1 - beta1^t), beta1, beta2 (8 bits: its root)
-  float g1, g2;                    // grad_scale times 1 - beta1 and sqrt(1 - beta2)
-  float inv_sqrt_bc2, eps;
+struct StepScalars {  // what every element needs; omb: 1 - beta
+  float gs, b1, omb1, b2, omb2;
+  float lr_wd1, step_size, inv_sqrt_bc2, eps;  // 1 - lr wd, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
 };
 
-// One special-function operation each, within 2^-23; a v below 2^-126 has root zero.
+// One special-function operation each, within 2^-23; with fp32 moments a v below 2^-126 has root zero.
 __device__ __forceinline__ float sqrt_approx(float x) {
   float r;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -230,6 +234,14 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
+}
+// Products that are added next, and their sums, each rounded by itself: scalar operations, since
+// packed ones are fused (a mul.rn.f32x2 with the addition after it, in some of the kernels).
+__device__ __forceinline__ float2 mul2_rn(float2 a, float b) {
+  return make_float2(__fmul_rn(a.x, b), __fmul_rn(a.y, b));
+}
+__device__ __forceinline__ float2 add2_rn(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
 }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -379,20 +391,35 @@ __device__ __forceinline__ void adam_block(const AdamEntry& t, const StepScalars
     unpack(w.m, m);
     unpack(w.v, v);
   }
-  // (1 - beta2) g'^2, and beta2 v where v is held as its root, are squares of scaled roots: the
-  // constants go into the scales
-  const float ms = BITS8 ? w.ms * s.b1 : s.b1, vs = BITS8 ? w.vs * s.b2 : s.b2;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const float2 g2 = mul2(g[q], both(s.g2));
-    m[q] = fma2(m[q], both(ms), mul2(g[q], both(s.g1)));
-    const float2 v_old = mul2(v[q], both(vs));
-    v[q] = BITS8 ? fma2(v_old, v_old, mul2(g2, g2)) : fma2(g2, g2, v_old);
-    r[q] = make_float2(sqrt_approx(v[q].x), sqrt_approx(v[q].y));
-    const float2 den = fma2(r[q], both(s.inv_sqrt_bc2), both(s.eps));
-    const float2 upd = mul2(mul2(m[q], both(s.neg_step)),
-                            make_float2(rcp_approx(den.x), rcp_approx(den.y)));
-    p[q] = fma2(p[q], both(s.lr_wd1), upd);
+    const float2 gv = mul2(g[q], both(s.gs));
+    if (BITS8 || PARAMS == kAlone) {
+      // every operation rounded by itself, in the order of the formulas: see the top of the file
+      if (BITS8) {
+        m[q] = mul2(m[q], both(w.ms));
+        v[q] = mul2(v[q], both(w.vs));
+        v[q] = mul2(v[q], v[q]);
+      }
+      m[q] = add2_rn(mul2_rn(m[q], s.b1), mul2_rn(gv, s.omb1));
+      const float2 gg = mul2(gv, both(s.omb2));
+      v[q] = add2_rn(mul2_rn(v[q], s.b2), make_float2(__fmul_rn(gg.x, gv.x), __fmul_rn(gg.y, gv.y)));
+      r[q] = make_float2(__fsqrt_rn(v[q].x), __fsqrt_rn(v[q].y));
+    } else {
+      m[q] = fma2(m[q], both(s.b1), mul2(gv, both(s.omb1)));
+      v[q] = fma2(v[q], both(s.b2), mul2(mul2(gv, both(s.omb2)), gv));
+      r[q] = make_float2(sqrt_approx(v[q].x), sqrt_approx(v[q].y));
+    }
+    if (PARAMS == kAlone) {
+      const float2 num = mul2(both(s.step_size), m[q]), keep = mul2_rn(p[q], s.lr_wd1);
+      const float2 den = add2_rn(mul2_rn(r[q], s.inv_sqrt_bc2), both(s.eps));
+      p[q] = make_float2(__fsub_rn(keep.x, __fdiv_rn(num.x, den.x)), __fsub_rn(keep.y, __fdiv_rn(num.y, den.y)));
+    } else {
+      const float2 den = fma2(r[q], both(s.inv_sqrt_bc2), both(s.eps));
+      const float2 upd = mul2(mul2(m[q], both(-s.step_size)),
+                              make_float2(rcp_approx(den.x), rcp_approx(den.y)));
+      p[q] = fma2(p[q], both(s.lr_wd1), upd);
+    }
   }
   uint32_t h[4];
   if (BITS8 || PARAMS == kAlone) {
@@ -422,8 +449,10 @@ __device__ __forceinline__ void adam_block(const AdamEntry& t, const StepScalars
     const float ra = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(ra4)));
     // a block below 2^-96 (its reciprocal could overflow) is kept as zeros: codes and scale
     const float m_max = ma < 0x1p-96f ? 0.f : ma, r_max = ra < 0x1p-96f ? 0.f : ra;
-    const float m_inv = m_max > 0.f ? 448.f * rcp_approx(m_max) : 0.f;
-    const float r_inv = r_max > 0.f ? 448.f * rcp_approx(r_max) : 0.f;
+    // lane 0 takes m's reciprocal, the others r's: one exact division for both
+    const float x_max = lane == 0 ? m_max : r_max;
+    const float x_inv = x_max > 0.f ? __frcp_rn(x_max) * 448.f : 0.f;
+    const float m_inv = __shfl_sync(kFull, x_inv, 0), r_inv = __shfl_sync(kFull, x_inv, 1);
     const uint32_t least = r_max > 0.f ? 1u << 24 : 0u;  // a nonzero r's smallest code
     uint32_t mc[4], rc[4];
 #pragma unroll
@@ -501,26 +530,30 @@ __global__ void __launch_bounds__(kOptThreads, BITS8 ? 4 : 3)
   const float gs = sc.grad_scale != nullptr ? *sc.grad_scale : 1.0f;
   if (!isfinite(gs)) return;  // the whole step is left out
   int step = sc.step;
-  float inv_bc1 = sc.inv_bc1, inv_sqrt_bc2 = sc.inv_sqrt_bc2;
-  if (sc.step_dev != nullptr) {
-    step = *sc.step_dev;
+  double rate = sc.rate;
+  float step_size = sc.step_size, inv_sqrt_bc2 = sc.inv_sqrt_bc2;
+  if (sc.step_dev != nullptr || sc.lr_dev != nullptr) {
+    if (sc.step_dev != nullptr) step = *sc.step_dev;
+    if (sc.lr_dev != nullptr) rate = *sc.lr_dev;
     if (step < 1) return;
     if (threadIdx.x == 0) {
-      s_bc[0] = static_cast<float>(1.0 / (1.0 - pow(sc.beta1, static_cast<double>(step))));
-      s_bc[1] = static_cast<float>(1.0 / sqrt(1.0 - pow(sc.beta2, static_cast<double>(step))));
+      s_bc[0] = static_cast<float>(rate / (1.0 - pow(sc.beta1, static_cast<double>(step))));
+      s_bc[1] = 1.0f / static_cast<float>(sqrt(1.0 - pow(sc.beta2, static_cast<double>(step))));
     }
     __syncthreads();
-    inv_bc1 = s_bc[0];
+    step_size = s_bc[0];
     inv_sqrt_bc2 = s_bc[1];
   }
-  const float lr = sc.lr_dev != nullptr ? *sc.lr_dev : sc.lr;
   for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
     const AdamEntry& t = tab.e[find_entry(tab.e, tab.n, c)];
     const int64_t tile = static_cast<int64_t>(c - t.chunk0) * tab.chunk_tiles;
     const int64_t tiles = (t.numel - 1) / (kTileBlocks * kQBlock) + 1;
     const int n = static_cast<int>(min(tiles - tile, static_cast<int64_t>(tab.chunk_tiles)));
-    const StepScalars s{1.0f - lr * t.weight_decay, -lr * inv_bc1,     sc.b1,        BITS8 ? sc.root_b2 : sc.b2,
-                        gs * sc.omb1,               gs * sc.root_omb2, inv_sqrt_bc2, sc.eps};
+    const StepScalars s{gs,      sc.b1,
+                        sc.omb1, sc.b2,
+                        sc.omb2, static_cast<float>(1.0 - rate * static_cast<double>(t.weight_decay)),
+                        step_size, inv_sqrt_bc2,
+                        sc.eps};
     const uint32_t key =
         mix32(mix32(static_cast<uint32_t>(t.index) * 0x632BE5ABu + sc.seed) +
               static_cast<uint32_t>(step) * 0x9E3779B1u);
@@ -663,19 +696,18 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int n, const moe_adamw
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
   AdamScalars sc{};
-  sc.lr = static_cast<float>(cfg.lr);
+  sc.rate = cfg.lr;
   sc.b1 = static_cast<float>(cfg.beta1);
   sc.omb1 = static_cast<float>(1.0 - cfg.beta1);
   sc.b2 = static_cast<float>(cfg.beta2);
-  sc.root_b2 = static_cast<float>(sqrt(cfg.beta2));
-  sc.root_omb2 = static_cast<float>(sqrt(1.0 - cfg.beta2));
+  sc.omb2 = static_cast<float>(1.0 - cfg.beta2);
   sc.eps = static_cast<float>(cfg.eps);
   sc.beta1 = cfg.beta1;
   sc.beta2 = cfg.beta2;
   sc.step = cfg.step;
   if (cfg.step_dev == nullptr) {
-    sc.inv_bc1 = static_cast<float>(1.0 / (1.0 - pow(cfg.beta1, cfg.step)));
-    sc.inv_sqrt_bc2 = static_cast<float>(1.0 / sqrt(1.0 - pow(cfg.beta2, cfg.step)));
+    sc.step_size = static_cast<float>(cfg.lr / (1.0 - pow(cfg.beta1, cfg.step)));
+    sc.inv_sqrt_bc2 = 1.0f / static_cast<float>(sqrt(1.0 - pow(cfg.beta2, cfg.step)));
   }
   sc.seed = cfg.seed;
   sc.step_dev = cfg.step_dev;

@@ -463,6 +463,64 @@ def test_adamw_step_and_rate_on_the_device_replayed():
         assert float((x != y).float().mean()) < 5e-3 and torch.allclose(x, y, rtol=0.13, atol=2e-4), k
 
 
+@pytest.mark.parametrize("kind", [k for k in KINDS if k[2] == 8 or k[0] == "bf16"],
+                         ids=lambda k: f"{k[0]}-{str(k[1])[6:]}-{k[2]}")
+def test_adamw_rounded_states_bit_by_bit(kind):
+    """Where codes are kept, every fp32 operation is rounded by itself in the order of the formulas: the
+    same lines in fp32 tensor operations give the same bits, over several steps."""
+    n, lr, b1, b2, eps, wd, seed = 128 * 20000, 3e-4, 0.9, 0.999, 1e-8, 0.1, 11
+    t = make_tensor(n, kind, seed=21)
+    t["grad"] = t["grad"].float().to(kind[1])
+    scale = torch.tensor([0.37], device="cuda")
+    w = (t["master"] if kind[0] == "master" else t["param"].float()).clone()
+    m, v = t["m"].clone(), t["v"].clone()
+    ms, vs = (t["m_scale"].clone(), t["v_scale"].clone()) if kind[2] == 8 else (None, None)
+    plan = moe.adamw_plan([descriptor(t, wd)])
+
+    def codes(x, words, keep):
+        top = x.view(-1, 128).abs().amax(1, keepdim=True)
+        x = x.view(-1, 128) * (448 / top)
+        y = x.abs()
+        small = y < 2.0 ** -6
+        y = torch.where(small, y + 2.0 ** -6, y)
+        c = ((y.view(torch.int32) + words.view(-1, 128) * 16 + 8) >> 20) - 960 - 8 * small
+        c = c.clamp(max=126)
+        c = torch.where(x > 0, c.clamp(min=1), c) if keep else c
+        return (c + 128 * (x < 0)).to(torch.uint8).view(torch.float8_e4m3fn).view(-1), (top / 448)[:, 0]
+
+    for step in (5, 6, 7):
+        moe.adamw_step(plan, step, lr=lr, betas=(b1, b2), eps=eps, seed=seed, grad_scale=scale)
+        um, uv, up = (torch.tensor(u, dtype=torch.int32, device="cuda") for u in oracle.random_bits(n, seed, step, 0))
+        g = t["grad"].float() * scale
+        m32 = m.float() if ms is None else (m.float().view(-1, 128) * ms[:, None]).view(-1)
+        v32 = v.float() if vs is None else (v.float().view(-1, 128) * vs[:, None]).square().view(-1)
+        m32 = b1 * m32 + (1 - b1) * g
+        v32 = b2 * v32 + (1 - b2) * g * g
+        r = v32.sqrt()
+        # the quotient on the host: the framework's elementwise division is not to nearest everywhere
+        f = np.float32
+        inv = f(1) / f(np.sqrt(1 - b2 ** step))
+        upd = f(lr / (1 - b1 ** step)) * m32.cpu().numpy() / (r.cpu().numpy() * inv + f(eps))
+        w = w.cpu().numpy() * f(1 - lr * float(f(wd))) - upd
+        assert w.dtype == f
+        w = torch.tensor(w, device="cuda")
+        if kind[2] == 8:
+            m, ms = codes(m32, um, False)
+            v, vs = codes(r, uv, True)
+            assert torch.equal(t["m_scale"], ms) and torch.equal(t["v_scale"], vs)
+        else:
+            m, v = m32, v32
+        assert torch.equal(t["m"].float(), m.float()) and torch.equal(t["v"].float(), v.float())
+        if kind[0] == "bf16":
+            w = ((w.view(torch.int32) + up) & -65536).view(torch.float32)
+            assert torch.equal(t["param"].float(), w)
+        else:
+            # the fp32 parameter rounds twice a step on either side (4 u of it together) and its update,
+            # below 3 lr here, has approximate square roots and quotients (32 u of it): three steps
+            torch.testing.assert_close(t["master"] if kind[0] == "master" else t["param"], w, rtol=3 * 4 * U,
+                                       atol=3 * 32 * U * 3 * lr)
+
+
 def test_adamw_moments_in_8_bits_keep_their_expectation():
     """From one state and 400 seeds: the mean of the stored second moment's root is its exact value.
     A value's spread is at most half a spacing (2^-4 of it): the mean of 400 is within 5 x
