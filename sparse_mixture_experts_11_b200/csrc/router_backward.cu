@@ -250,9 +250,9 @@ constexpr int kFlush = 8;           // stages of a chain: 8 * 2 steps * 3 terms 
 constexpr int kXTileT = 128, kXTileC = 256;
 
 // Shared-memory descriptor of an MN-major operand of kKb k rows: groups of 8 k rows are 1024 bytes
-// (stride offset), blocks of 64 MN elements one box (leading offset).
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(kBox >> 4) << 16) |
+// (stride offset), blocks of 64 MN elements `lead` bytes apart (leading offset).
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lead) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lead >> 4) << 16) |
          (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 // K-major operand with 64-byte rows (32 elements, 64B-swizzled): groups of 8 rows are 512 bytes.
@@ -473,6 +473,10 @@ __device__ __forceinline__ void tc_setup(TcShared& sh, int warp, uint32_t column
   tc_fence_after_sync();
 }
 
+// A stage's operands come in few, large copies: one for x (its columns as blocks of 64: box [4][32 t][64]),
+// one for each 64 experts' three terms. (A copy of 4 KB for each 64 columns and term took 150 to 240
+// cycles of the one thread that issues them, and bound both GEMMs: 166 us here, 243 us below, at
+// T = 16384, N = 256, d = 7168.)
 // Weight gradient (the axis d on the MMA's rows: a warp's 32 lanes store 128 consecutive bytes of
 // dW from registers): one CTA for 256 columns of d, NU experts and one range of the tokens. A: x [t][c],
 // MN-major, two row blocks of 128 columns; B: the terms of dL [t][n], MN-major. D[c][n]: two chains
@@ -499,7 +503,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int range = static_cast<int>(blockIdx.x) / (n_tiles * c_tiles);
   const int64_t t0 = range * chunk, t1 = min(T, t0 + chunk);
   const int nkb = static_cast<int>((t1 - t0 + kKb - 1) / kKb);
-  const int a_boxes = min(kWTile / 64, (d - c0) / 64);  // d is a multiple of 64
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t last = l2_policy_evict_last();
@@ -514,13 +517,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t fb = smem_u32(&sh.full[s]);
         const uint32_t dst = base + s * kStageBytes, b_dst = dst + kWTile / 64 * kBox;
         const int t = static_cast<int>(t0) + it * kKb;
-        mbar_arrive_expect_tx(fb, (a_boxes + 3 * kBoxes) * kBox);
-        for (int i = 0; i < a_boxes; ++i) tma_load_2d(dst + i * kBox, &tm_x, fb, c0 + 64 * i, t, last);
+        mbar_arrive_expect_tx(fb, kStageBytes);
+        tma_load_3d(dst, &tm_x, fb, 0, t, c0 / 64, last);
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
-#pragma unroll
-          for (int i = 0; i < kBoxes; ++i)
-            tma_load_3d(b_dst + (k * kBoxes + i) * kBox, &tm_dl, fb, n0 + 64 * i, t, k, last);
+        for (int i = 0; i < kBoxes; ++i) tma_load_3d(b_dst + i * 3 * kBox, &tm_dl, fb, n0 + 64 * i, t, 0, last);
       }
       if (!ok) {
         sh.abort = 1;
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 1) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, NU) | (1u << 15) | (1u << 16);
-    const int blocks = (a_boxes + 1) / 2;  // row blocks of 128 columns
+    const int blocks = d - c0 > 128 ? 2 : 1;  // row blocks of 128 columns
     bool ok = true, issued = false;
     for (int it = 0; it < nkb; ++it) {
       const int s = it % kStages, u = it / kFlush;
@@ -556,8 +556,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int kk = 0; kk < kKb / 16; ++kk)
 #pragma unroll
             for (int k = 0; k < 3; ++k)
-              tc_mma_f16(dst + m * NU, desc_mn(a + 2 * m * kBox + kk * 2048),
-                         desc_mn(b + k * kBoxes * kBox + kk * 2048), idesc, it % kFlush > 0 || kk > 0 || k > 0);
+              tc_mma_f16(dst + m * NU, desc_mn(a + 2 * m * kBox + kk * 2048, kBox),
+                         desc_mn(b + k * kBox + kk * 2048, 3 * kBox), idesc, it % kFlush > 0 || kk > 0 || k > 0);
         tc_commit(smem_u32(&sh.empty[s]));
         if (it % kFlush == kFlush - 1 || it == nkb - 1) tc_commit(smem_u32(&sh.tfull[u & 1]));
       }
@@ -662,7 +662,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
         const int c0 = static_cast<int>(t % c_tiles) * kXTileC;
         const int r0 = static_cast<int>(t / c_tiles) * kXTileT;
-        const int boxes = min(kXTileC / 64, (d - c0) / 64);  // d is a multiple of 64
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const int s = it % kXStages;
           if (!mbar_wait(smem_u32(&sh.empty[s]), ((it / kXStages) & 1) ^ 1u, timeout_ns, &sh.abort)) {
@@ -671,12 +670,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           const uint32_t fb = smem_u32(&sh.full[s]);
           const uint32_t a = base + s * kXStageBytes, b = a + 2 * kABytes;
-          mbar_arrive_expect_tx(fb, 2 * (kABytes + boxes * kBox));
-          for (int k = 0; k < 2; ++k) {
-            tma_load_3d(a + k * kABytes, &tm_dl, fb, kb * kKb, r0, k, last);
-            for (int i = 0; i < boxes; ++i)
-              tma_load_3d(b + k * kBBytes + i * kBox, &tm_w, fb, c0 + 64 * i, kb * kKb, k, last);
-          }
+          mbar_arrive_expect_tx(fb, kXStageBytes);
+          tma_load_3d(a, &tm_dl, fb, kb * kKb, r0, 0, last);
+          tma_load_4d(b, &tm_w, fb, 0, kb * kKb, c0 / 64, 0, last);
         }
       }
       if (!ok) {
@@ -715,7 +711,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int k = 0; k < 3; ++k)  // terms (0, 0), (0, 1), (1, 0)
               tc_mma_f16(tmem + buf * kXTileC, desc_k64(a + (k == 2 ? kABytes : 0) + kk * 32),
-                         desc_mn(b + (k == 1 ? kBBytes : 0) + kk * 2048), idesc, kb > 0 || kk > 0 || k > 0);
+                         desc_mn(b + (k == 1 ? kBBytes : 0) + kk * 2048, kBox), idesc, kb > 0 || kk > 0 || k > 0);
           tc_commit(smem_u32(&sh.empty[s]));
         }
         issued = true;
@@ -845,9 +841,10 @@ cudaError_t launch_tc(const RouterBackwardArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (want_w) {
     CUtensorMap mx, mdl;
-    const uint64_t xd[2] = {d, T}, xs[1] = {d * 2}, ld[3] = {np, T, 3}, ls[2] = {np * 2, T * np * 2};
-    const uint32_t xb[2] = {64, kKb}, lb[3] = {64, kKb, 1};
-    if (!make_map(&mx, a.x, 2, xd, xs, xb) || !make_map(&mdl, dl_terms, 3, ld, ls, lb)) return cudaErrorInvalidValue;
+    // x as [d / 64][T][64]
+    const uint64_t xd[3] = {64, T, d / 64}, xs[2] = {d * 2, 128}, ld[3] = {np, T, 3}, ls[2] = {np * 2, T * np * 2};
+    const uint32_t xb[3] = {64, kKb, kWTile / 64}, lb[3] = {64, kKb, 3};
+    if (!make_map(&mx, a.x, 3, xd, xs, xb) || !make_map(&mdl, dl_terms, 3, ld, ls, lb)) return cudaErrorInvalidValue;
     e = p.nu == 16   ? launch_wgrad<16>(mx, mdl, part, a, p, s)
         : p.nu == 32 ? launch_wgrad<32>(mx, mdl, part, a, p, s)
         : p.nu == 64 ? launch_wgrad<64>(mx, mdl, part, a, p, s)
@@ -858,11 +855,13 @@ cudaError_t launch_tc(const RouterBackwardArgs& a, cudaStream_t s) {
     CUtensorMap mw, mdl, mo;
     const uint64_t od[2] = {d, T}, os[1] = {d * 4};
     const uint32_t ob[2] = {32, 32};
-    const uint64_t wd[3] = {d, static_cast<uint64_t>(a.N), 2}, wst[2] = {d * 2, static_cast<uint64_t>(a.N) * d * 2};
+    // W_r's terms as [2][d / 64][N][64]
+    const uint64_t wd[4] = {64, static_cast<uint64_t>(a.N), d / 64, 2};
+    const uint64_t wst[3] = {d * 2, 128, static_cast<uint64_t>(a.N) * d * 2};
     const uint64_t ld[3] = {np, T, 2}, ls[2] = {np * 2, T * np * 2};
-    const uint32_t wb[3] = {64, kKb, 1}, lb[3] = {kKb, kXTileT, 1};
+    const uint32_t wb[4] = {64, kKb, kXTileC / 64, 2}, lb[3] = {kKb, kXTileT, 2};
     // 16-bit elements either way: the copy does not look at the format
-    if (!make_map(&mw, w_terms, 3, wd, wst, wb) ||
+    if (!make_map(&mw, w_terms, 4, wd, wst, wb) ||
         !make_map(&mdl, dl16, 3, ld, ls, lb, CU_TENSOR_MAP_SWIZZLE_64B) ||
         !make_map_f32(&mo, a.d_x, 2, od, os, ob))
       return cudaErrorInvalidValue;
