@@ -261,6 +261,15 @@ __device__ __forceinline__ uint64_t desc_k64(uint32_t addr) {
          (static_cast<uint64_t>(512u >> 4) << 32) | (1ull << 46) | (4ull << 61);
 }
 
+// True on one lane, always the same one. The MMA warp runs its loops as a whole and elects a lane for
+// each instruction: the operands stay warp-uniform, where a branch on the lane around the loops
+// makes every one of them move to a uniform register first (about 100 cycles an MMA).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 struct TcPlan {
   int np;  // N rounded up to 8: row length of dL's terms
   int nu;  // experts of a weight-gradient tile (MMA columns): 16, 32, 64 or 128
@@ -548,16 +557,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         break;
       }
       tc_fence_after_sync();
-      if (lane == 0) {
-        const uint32_t a = base + s * kStageBytes, b = a + kWTile / 64 * kBox;
-        const uint32_t dst = tmem + (u & 1) * 2 * NU;
-        for (int m = 0; m < blocks; ++m)
+      const uint64_t a = desc_mn(base + s * kStageBytes, kBox);
+      const uint64_t b = desc_mn(base + s * kStageBytes + kWTile / 64 * kBox, 3 * kBox);
+      const uint32_t dst = tmem + (u & 1) * 2 * NU;
+      const bool add = it % kFlush > 0;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (m < blocks) {
 #pragma unroll
           for (int kk = 0; kk < kKb / 16; ++kk)
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
-              tc_mma_f16(dst + m * NU, desc_mn(a + 2 * m * kBox + kk * 2048, kBox),
-                         desc_mn(b + k * kBox + kk * 2048, 3 * kBox), idesc, it % kFlush > 0 || kk > 0 || k > 0);
+            for (int k = 0; k < 3; ++k)  // address offsets in the descriptors, in 16-byte units
+              if (elect_one())
+                tc_mma_f16(dst + m * NU, a + ((2 * m * kBox + kk * 2048) >> 4), b + ((k * kBox + kk * 2048) >> 4), idesc,
+                           kk > 0 || k > 0 ? 1u : add);
+        }
+      }
+      if (elect_one()) {
         tc_commit(smem_u32(&sh.empty[s]));
         if (it % kFlush == kFlush - 1 || it == nkb - 1) tc_commit(smem_u32(&sh.tfull[u & 1]));
       }
@@ -568,7 +584,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sh.abort = 1;
       report_error(status, MOE_ERR_TIMEOUT);
     }
-    if (issued && lane == 0) {  // every MMA has finished before the TMEM is freed
+    if (issued && elect_one()) {  // every MMA has finished before the TMEM is freed
       tc_commit(smem_u32(&sh.done));
       mbar_wait(smem_u32(&sh.done), 0, kDrainTimeoutNs, nullptr);
     }
@@ -704,27 +720,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           break;
         }
         tc_fence_after_sync();
-        if (lane == 0) {
-          const uint32_t a = base + s * kXStageBytes, b = a + 2 * kABytes;
-          const int steps = min(kKb / 16, (N - kb * kKb + 15) / 16);
-          for (int kk = 0; kk < steps; ++kk)
+        const uint64_t a = desc_k64(base + s * kXStageBytes), b = desc_mn(base + s * kXStageBytes + 2 * kABytes, kBox);
+        const int steps = (N - kb * kKb + 15) / 16;
+#pragma unroll
+        for (int kk = 0; kk < kKb / 16; ++kk) {
+          if (kk < steps) {
 #pragma unroll
             for (int k = 0; k < 3; ++k)  // terms (0, 0), (0, 1), (1, 0)
-              tc_mma_f16(tmem + buf * kXTileC, desc_k64(a + (k == 2 ? kABytes : 0) + kk * 32),
-                         desc_mn(b + (k == 1 ? kBBytes : 0) + kk * 2048, kBox), idesc, kb > 0 || kk > 0 || k > 0);
-          tc_commit(smem_u32(&sh.empty[s]));
+              if (elect_one())
+                tc_mma_f16(tmem + buf * kXTileC, a + (((k == 2 ? kABytes : 0) + kk * 32) >> 4),
+                           b + (((k == 1 ? kBBytes : 0) + kk * 2048) >> 4), idesc, kk > 0 || k > 0 ? 1u : kb > 0);
+          }
         }
+        if (elect_one()) tc_commit(smem_u32(&sh.empty[s]));
         issued = true;
         __syncwarp();
       }
       if (!ok) break;
-      if (lane == 0) tc_commit(smem_u32(&sh.tfull[buf]));
+      if (elect_one()) tc_commit(smem_u32(&sh.tfull[buf]));
     }
     if (!ok && lane == 0) {
       sh.abort = 1;
       report_error(status, MOE_ERR_TIMEOUT);
     }
-    if (issued && lane == 0) {
+    if (issued && elect_one()) {
       tc_commit(smem_u32(&sh.done));
       mbar_wait(smem_u32(&sh.done), 0, kDrainTimeoutNs, nullptr);
     }
