@@ -238,15 +238,14 @@ cudaError_t launch_sum(const float* part_w, const float* part_b, const RouterBac
 //            terms of each would need six products.
 // The accumulator of the MMA truncates: measured, a chain of additions loses 1.1e-8 of its value a
 // step of 16 products. dx has 3 N / 16 <= 48 steps. dW's chains would be thousands; they are cut
-// after 48 steps (kFlush stages) and summed in fp32 registers by the epilogue warps, while the
-// other half of TMEM takes the next chain.
+// after 48 steps and summed in fp32 registers by the epilogue warps, while the other half of
+// TMEM takes the next chain.
 constexpr int kKb = 32;             // reduction elements of a stage
 constexpr int kBox = 64 * kKb * 2;  // one TMA box of an MN-major operand: 64 MN x 32 k, 128B-swizzled
 constexpr int kTcThreads = 320;     // TMA producer, MMA issuer, eight epilogue warps
 constexpr int kTcMinSmem = 120 * 1024;  // one CTA an SM: the TMEM is not shared
 constexpr int kTcMaxSmem = 226 * 1024;  // dynamic; barriers beside it
-constexpr int kWTile = 256;         // columns of d a CTA of the weight gradient owns (two MMA row blocks)
-constexpr int kFlush = 8;           // stages of a chain: 8 * 2 steps * 3 terms = 48
+constexpr int kWTile = 256;         // columns of d a CTA of the weight gradient owns
 constexpr int kXTileT = 128, kXTileC = 256;
 
 // Shared-memory descriptor of an MN-major operand of kKb k rows: groups of 8 k rows are 1024 bytes
@@ -254,6 +253,12 @@ constexpr int kXTileT = 128, kXTileC = 256;
 __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lead) {
   return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lead >> 4) << 16) |
          (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// The same in blocks of 32 MN elements (64-byte rows, 64B-swizzled): groups of 8 k rows are 512 bytes,
+// blocks 64 * kKb.
+__device__ __forceinline__ uint64_t desc_mn32(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((64u * kKb) >> 4) << 16) |
+         (static_cast<uint64_t>(512u >> 4) << 32) | (1ull << 46) | (4ull << 61);
 }
 // K-major operand with 64-byte rows (32 elements, 64B-swizzled): groups of 8 rows are 512 bytes.
 __device__ __forceinline__ uint64_t desc_k64(uint32_t addr) {
@@ -272,23 +277,27 @@ __device__ __forceinline__ bool elect_one() {
 
 struct TcPlan {
   int np;  // N rounded up to 8: row length of dL's terms
-  int nu;  // experts of a weight-gradient tile (MMA columns): 16, 32, 64 or 128
+  int group;  // experts of a weight-gradient tile: 32, 64 or 128
+  int planes;  // planes of partial sums a range leaves: 3, 2, 1
   int n_tiles, c_tiles, chunks;
   int64_t chunk;  // tokens of a range of the weight gradient, a multiple of kKb
   int split_rows, split_ctas;  // tokens a CTA of split_dl_kernel takes, and how many such CTAs
   size_t dl16_bytes, dl_bytes, w_bytes, exp_bytes, part_bytes, bias_bytes;
   size_t total() const { return dl16_bytes + dl_bytes + w_bytes + exp_bytes + part_bytes + bias_bytes; }
 };
-__host__ __device__ constexpr int w_stage_bytes(int nu) { return (kWTile / 64 + 3 * ((nu + 63) / 64)) * kBox; }
-__host__ __device__ constexpr int w_stages(int nu) {
-  return (kTcMaxSmem - 1024) / w_stage_bytes(nu) < 8 ? (kTcMaxSmem - 1024) / w_stage_bytes(nu) : 8;
+// A stage of the weight gradient: dL's terms (32 or 64 experts: three and a plane of zeros), then x.
+__host__ __device__ constexpr int w_a_bytes(int group) { return (group == 32 ? 4 * 32 : group == 64 ? 4 * 64 : 3 * 128) * kKb * 2; }
+__host__ __device__ constexpr int w_stage_bytes(int group) { return w_a_bytes(group) + kWTile * kKb * 2; }
+__host__ __device__ constexpr int w_stages(int group) {
+  return (kTcMaxSmem - 1024) / w_stage_bytes(group) < 8 ? (kTcMaxSmem - 1024) / w_stage_bytes(group) : 8;
 }
 
 TcPlan make_tc_plan(int64_t T, int N, int d) {
   TcPlan p{};
   p.np = (N + 7) / 8 * 8;
-  p.nu = N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : 128;
-  p.n_tiles = (N + p.nu - 1) / p.nu;
+  p.group = N <= 32 ? 32 : N <= 64 ? 64 : 128;
+  p.planes = p.group == 32 ? 3 : p.group == 64 ? 2 : 1;
+  p.n_tiles = (N + p.group - 1) / p.group;
   p.c_tiles = (d + kWTile - 1) / kWTile;
   // Token ranges: the fewest tokens a CTA in all (whole waves of 148 CTAs), where starting and
   // ending a CTA costs about what 128 tokens do
@@ -310,7 +319,7 @@ TcPlan make_tc_plan(int64_t T, int N, int d) {
   p.dl_bytes = r256(static_cast<size_t>(3) * T * p.np * 2);
   p.w_bytes = r256(static_cast<size_t>(2) * N * d * 2);
   p.exp_bytes = r256(static_cast<size_t>(N) * 4) + r256(static_cast<size_t>(T) * 4);
-  p.part_bytes = r256(static_cast<size_t>(p.chunks) * N * d * 4);
+  p.part_bytes = r256(static_cast<size_t>(p.chunks) * p.planes * N * d * 4);
   p.bias_bytes = r256(static_cast<size_t>(p.split_ctas) * N * 4);
   return p;
 }
@@ -482,32 +491,38 @@ __device__ __forceinline__ void tc_setup(TcShared& sh, int warp, uint32_t column
   tc_fence_after_sync();
 }
 
-// A stage's operands come in few, large copies: one for x (its columns as blocks of 64: box [4][32 t][64]),
-// one for each 64 experts' three terms. (A copy of 4 KB for each 64 columns and term took 150 to 240
-// cycles of the one thread that issues them, and bound both GEMMs: 166 us here, 243 us below, at
-// T = 16384, N = 256, d = 7168.)
-// Weight gradient (the axis d on the MMA's rows: a warp's 32 lanes store 128 consecutive bytes of
-// dW from registers): one CTA for 256 columns of d, NU experts and one range of the tokens. A: x [t][c],
-// MN-major, two row blocks of 128 columns; B: the terms of dL [t][n], MN-major. D[c][n]: two chains
-// in TMEM, buffer u at columns [2 NU u, 2 NU (u + 1)), row block m at + NU m. The range's sum goes to
-// part [range][N][d].
-template <int NU>
+// Weight gradient: one CTA for 256 columns of d, GROUP experts and one range of the tokens. A: the
+// terms of dL [t][n], MN-major; B: x [t][c], MN-major; D[n][c] on 128 rows:
+//   32 experts   rows 0-31 are the high terms' products, 32-63 the middle, 64-95 the low ones
+//                (one MMA a k step; the fourth plane is zeros);
+//   64 experts   rows 0-63 high and low, 64-127 middle (two MMAs: planes 0 and 1, planes 2 and zeros);
+//   128 experts  all three terms in each row (three MMAs).
+// What bounds it is shared memory's bandwidth to the tensor core, half of the usual for MN-major
+// operands as measured: experts on the rows and 256 columns an MMA read 12 KB for 128 x 256 x 16
+// products. (d on the rows, one MMA for each term, 128 columns of d and 128 experts: 160 us at T =
+// 16384, N = 256, d = 7168; for 32 experts, d = 2880 29 us.)
+// A stage's operands come in few, large copies: one for x (box [4][32 t][64 c]), one for the terms
+// (two with 128 experts). Two chains in TMEM, 256 columns each. The range's sums, a plane for each
+// group of rows, leave through shared memory: part [range][plane][N][d].
+template <int GROUP>
 __global__ void __launch_bounds__(kTcThreads, 1)
     router_wgrad_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_dl,
-                        float* __restrict__ part, int64_t T, int N, int d, int c_tiles, int n_tiles, int64_t chunk,
-                        int* status, uint64_t timeout_ns) {
-  constexpr int kStages = w_stages(NU), kStageBytes = w_stage_bytes(NU), kBoxes = (NU + 63) / 64;
-  constexpr uint32_t kColumns = 4 * NU;
+                        const __grid_constant__ CUtensorMap tm_part, int64_t T, int N, int d, int c_tiles,
+                        int n_tiles, int64_t chunk, int* status, uint64_t timeout_ns) {
+  constexpr int kStages = w_stages(GROUP), kStageBytes = w_stage_bytes(GROUP), kABytes = w_a_bytes(GROUP);
+  constexpr int kPlanes = GROUP == 32 ? 3 : GROUP == 64 ? 2 : 1;
+  constexpr int kFlush = GROUP == 32 ? 24 : GROUP == 64 ? 12 : 8;  // stages of a chain: 48 steps
+  constexpr int kMmas = GROUP == 32 ? 1 : GROUP == 64 ? 2 : 3;     // a k step
   extern __shared__ __align__(1024) uint8_t dyn_smem[];
   __shared__ TcShared sh;
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(dyn_smem) + 1023u) & ~1023u;
-  tc_setup(sh, warp, kColumns);
+  tc_setup(sh, warp, 512);
   pdl_wait();
   const uint32_t tmem = sh.tmem;
   // neighbouring CTAs share a range and columns of x
-  const int n0 = static_cast<int>(blockIdx.x) % n_tiles * NU;
+  const int n0 = static_cast<int>(blockIdx.x) % n_tiles * GROUP;
   const int c0 = static_cast<int>(blockIdx.x) / n_tiles % c_tiles * kWTile;
   const int range = static_cast<int>(blockIdx.x) / (n_tiles * c_tiles);
   const int64_t t0 = range * chunk, t1 = min(T, t0 + chunk);
@@ -524,12 +539,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           break;
         }
         const uint32_t fb = smem_u32(&sh.full[s]);
-        const uint32_t dst = base + s * kStageBytes, b_dst = dst + kWTile / 64 * kBox;
+        const uint32_t dst = base + s * kStageBytes;
         const int t = static_cast<int>(t0) + it * kKb;
         mbar_arrive_expect_tx(fb, kStageBytes);
-        tma_load_3d(dst, &tm_x, fb, 0, t, c0 / 64, last);
-#pragma unroll
-        for (int i = 0; i < kBoxes; ++i) tma_load_3d(b_dst + i * 3 * kBox, &tm_dl, fb, n0 + 64 * i, t, 0, last);
+        tma_load_3d(dst, &tm_dl, fb, n0, t, 0, last);
+        if (GROUP == 128) tma_load_3d(dst + 3 * kBox, &tm_dl, fb, n0 + 64, t, 0, last);
+        tma_load_3d(dst + kABytes, &tm_x, fb, 0, t, c0 / 64, last);
       }
       if (!ok) {
         sh.abort = 1;
@@ -539,8 +554,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_wait(smem_u32(&sh.full[i % kStages]), (i / kStages) & 1, kDrainTimeoutNs, nullptr);
     }
   } else if (warp == 1) {
-    constexpr uint32_t idesc = idesc_bf16_f32(128, NU) | (1u << 15) | (1u << 16);
-    const int blocks = d - c0 > 128 ? 2 : 1;  // row blocks of 128 columns
+    constexpr uint32_t idesc = idesc_bf16_f32(128, kWTile) | (1u << 15) | (1u << 16);
     bool ok = true, issued = false;
     for (int it = 0; it < nkb; ++it) {
       const int s = it % kStages, u = it / kFlush;
@@ -557,22 +571,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         break;
       }
       tc_fence_after_sync();
-      const uint64_t a = desc_mn(base + s * kStageBytes, kBox);
-      const uint64_t b = desc_mn(base + s * kStageBytes + kWTile / 64 * kBox, 3 * kBox);
-      const uint32_t dst = tmem + (u & 1) * 2 * NU;
+      const uint32_t st = base + s * kStageBytes;
+      const uint64_t a = GROUP == 32 ? desc_mn32(st) : GROUP == 64 ? desc_mn(st, kBox) : desc_mn(st, 3 * kBox);
+      const uint64_t b = desc_mn(st + kABytes, kBox);
       const bool add = it % kFlush > 0;
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        if (m < blocks) {
+      for (int kk = 0; kk < kKb / 16; ++kk)
 #pragma unroll
-          for (int kk = 0; kk < kKb / 16; ++kk)
-#pragma unroll
-            for (int k = 0; k < 3; ++k)  // address offsets in the descriptors, in 16-byte units
-              if (elect_one())
-                tc_mma_f16(dst + m * NU, a + ((2 * m * kBox + kk * 2048) >> 4), b + ((k * kBox + kk * 2048) >> 4), idesc,
-                           kk > 0 || k > 0 ? 1u : add);
-        }
-      }
+        for (int k = 0; k < kMmas; ++k)  // address offsets in the descriptors, in 16-byte units
+          if (elect_one())
+            tc_mma_f16(tmem + (u & 1) * kWTile,
+                       a + ((k * (GROUP == 64 ? 2 : 1) * kBox + kk * (GROUP == 32 ? 1024 : 2048)) >> 4),
+                       b + ((kk * 2048) >> 4), idesc, kk > 0 || k > 0 ? 1u : add);
       if (elect_one()) {
         tc_commit(smem_u32(&sh.empty[s]));
         if (it % kFlush == kFlush - 1 || it == nkb - 1) tc_commit(smem_u32(&sh.tfull[u & 1]));
@@ -589,13 +599,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_wait(smem_u32(&sh.done), 0, kDrainTimeoutNs, nullptr);
     }
   } else {
-    const int q = warp & 3;               // TMEM lane quadrant
-    const int m = (warp - 2) >> 2;        // row block
-    const int c = c0 + m * 128 + q * 32;  // the warp's first column of d; 32-column groups are whole
-    float acc[NU];
+    const int q = warp & 3;            // TMEM lane quadrant
+    const int half = (warp - 2) >> 2;  // columns [half * 128, half * 128 + 128) of the tile
+    const int plane = GROUP == 32 ? q : GROUP == 64 ? q >> 1 : 0;
+    const int n = n0 + (GROUP == 32 ? 0 : GROUP == 64 ? (q & 1) * 32 : q * 32);  // expert of lane 0
+    const int c = c0 + half * 128;
+    const bool mine = plane < kPlanes && n < N && c < d;
+    float acc[128];
 #pragma unroll
-    for (int i = 0; i < NU; ++i) acc[i] = 0.f;
-    const uint32_t row = tmem + (static_cast<uint32_t>(q * 32) << 16) + m * NU;
+    for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+    const uint32_t row = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
     bool ok = true;
     for (int u = 0; u * kFlush < nkb; ++u) {
       const bool got = mbar_wait(smem_u32(&sh.tfull[u & 1]), (u >> 1) & 1, timeout_ns, &sh.abort);
@@ -604,14 +617,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         break;
       }
       tc_fence_after_sync();
-      if (c < d) {
+      if (mine) {
 #pragma unroll
-        for (int n = 0; n < NU; n += 16) {
+        for (int j = 0; j < 128; j += 16) {
           uint32_t v[16];
-          tmem_ld_32x32b_x16(row + (u & 1) * 2 * NU + n, v);
+          tmem_ld_32x32b_x16(row + (u & 1) * kWTile + j, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[n + i] += __uint_as_float(v[i]);
+          for (int i = 0; i < 16; ++i) acc[j + i] += __uint_as_float(v[i]);
         }
       }
       tc_fence_before_sync();
@@ -620,18 +633,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (!ok) {
       sh.abort = 1;
       report_error(status, MOE_ERR_TIMEOUT);
-    } else if (c < d) {
-      float* out = part + (static_cast<int64_t>(range) * N + n0) * d + c + lane;
+    } else if (mine) {
+      // the last chain's barrier: every MMA is done, so the stages are free for the blocks that leave
+      const uint32_t stage = base + (warp - 2) * (32 * 32 * 4);
+      uint8_t* const stg = dyn_smem + (stage - smem_u32(dyn_smem));
 #pragma unroll
-      for (int i = 0; i < NU; ++i)
-        if (n0 + i < N) out[static_cast<int64_t>(i) * d] = acc[i];
+      for (int j = 0; j < 4; ++j) {
+        if (c + 32 * j < d) {
+          if (lane == 0) tma_store_wait_read();
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_float4(
+                acc[32 * j + 4 * i], acc[32 * j + 4 * i + 1], acc[32 * j + 4 * i + 2], acc[32 * j + 4 * i + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {  // experts past N are not written
+            tma_store_3d(&tm_part, stage, c + 32 * j, n, range * kPlanes + plane);
+            tma_store_commit();
+          }
+        }
+      }
+      if (lane == 0) tma_store_wait_all();
     }
   }
   tc_fence_before_sync();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, kColumns);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -816,17 +846,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // (4096, 2880, 32) 94, 33; (1024, 4096, 128) 126, 29. Below 64 tokens a row block of the MMA is half empty.
 bool use_tensor_cores(int64_t T, int N, int d) { return T >= 64 && static_cast<double>(T) * N * d >= 67108864.0; }
 
-template <int NU>
-cudaError_t launch_wgrad(const CUtensorMap& mx, const CUtensorMap& mdl, float* part, const RouterBackwardArgs& a,
-                         const TcPlan& p, cudaStream_t s) {
-  constexpr int smem = std::max(kTcMinSmem, w_stages(NU) * w_stage_bytes(NU) + 1024);
+template <int GROUP>
+cudaError_t launch_wgrad(const CUtensorMap& mx, const CUtensorMap& mdl, const CUtensorMap& mp,
+                         const RouterBackwardArgs& a, const TcPlan& p, cudaStream_t s) {
+  constexpr int smem = std::max(kTcMinSmem, w_stages(GROUP) * w_stage_bytes(GROUP) + 1024);
   static PerDeviceOnce once;
   const cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(router_wgrad_kernel<NU>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(router_wgrad_kernel<GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(router_wgrad_kernel<NU>, dim3(p.n_tiles * p.c_tiles * p.chunks), dim3(kTcThreads), smem, s, mx,
-                    mdl, part, static_cast<int64_t>(a.T), a.N, a.d, p.c_tiles, p.n_tiles, p.chunk, a.status,
+  return launch_pdl(router_wgrad_kernel<GROUP>, dim3(p.n_tiles * p.c_tiles * p.chunks), dim3(kTcThreads), smem, s,
+                    mx, mdl, mp, static_cast<int64_t>(a.T), a.N, a.d, p.c_tiles, p.n_tiles, p.chunk, a.status,
                     a.timeout_ns);
 }
 
@@ -859,15 +889,22 @@ cudaError_t launch_tc(const RouterBackwardArgs& a, cudaStream_t s) {
                  want_b ? bias_part : nullptr, static_cast<int64_t>(a.T), a.N, p.np, p.split_rows);
   if (e != cudaSuccess) return e;
   if (want_w) {
-    CUtensorMap mx, mdl;
+    CUtensorMap mx, mdl, mp;
     // x as [d / 64][T][64]
     const uint64_t xd[3] = {64, T, d / 64}, xs[2] = {d * 2, 128}, ld[3] = {np, T, 3}, ls[2] = {np * 2, T * np * 2};
-    const uint32_t xb[3] = {64, kKb, kWTile / 64}, lb[3] = {64, kKb, 3};
-    if (!make_map(&mx, a.x, 3, xd, xs, xb) || !make_map(&mdl, dl_terms, 3, ld, ls, lb)) return cudaErrorInvalidValue;
-    e = p.nu == 16   ? launch_wgrad<16>(mx, mdl, part, a, p, s)
-        : p.nu == 32 ? launch_wgrad<32>(mx, mdl, part, a, p, s)
-        : p.nu == 64 ? launch_wgrad<64>(mx, mdl, part, a, p, s)
-                     : launch_wgrad<128>(mx, mdl, part, a, p, s);
+    const uint64_t pd[3] = {d, static_cast<uint64_t>(a.N), static_cast<uint64_t>(p.chunks * p.planes)};
+    const uint64_t ps[2] = {d * 4, static_cast<uint64_t>(a.N) * d * 4};
+    const uint32_t xb[3] = {64, kKb, kWTile / 64}, pb[3] = {32, 32, 1};
+    // past the third term, and past N: zeros
+    const uint32_t lb[3] = {p.group == 32 ? 32u : 64u, kKb, p.group == 128 ? 3u : 4u};
+    if (!make_map(&mx, a.x, 3, xd, xs, xb) ||
+        !make_map(&mdl, dl_terms, 3, ld, ls, lb,
+                  p.group == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_f32(&mp, part, 3, pd, ps, pb))
+      return cudaErrorInvalidValue;
+    e = p.group == 32   ? launch_wgrad<32>(mx, mdl, mp, a, p, s)
+        : p.group == 64 ? launch_wgrad<64>(mx, mdl, mp, a, p, s)
+                        : launch_wgrad<128>(mx, mdl, mp, a, p, s);
     if (e != cudaSuccess) return e;
   }
   if (want_x) {
@@ -898,7 +935,7 @@ cudaError_t launch_tc(const RouterBackwardArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   if (!want_w && !want_b) return cudaSuccess;
-  return launch_sum(part, bias_part, a, p.chunks, p.split_ctas, s);
+  return launch_sum(part, bias_part, a, p.chunks * p.planes, p.split_ctas, s);
 }
 
 }  // namespace
