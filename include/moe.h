@@ -362,12 +362,14 @@ moe_status moe_balance_loss(const moe_dims* dims, const float* logits, const int
  *   d_w_router = d_logits^T x,  d_logit_bias = sum_t d_logits[t],  d_x = d_logits w_router
  *   x [T, d_model] bf16, w_router [N, d_model] fp32, d_logits [T, N] fp32
  *   d_x [T, d_model], d_w_router [N, d_model], d_logit_bias [N] fp32 (out), each may be NULL
+ *                and must not overlap the inputs
  *   accumulate   0: the outputs are written; 1: added to, as after moe_backward, whose outputs
  *                of the same names have the same shapes
  *   ws, ws_bytes workspace (moe_router_backward_workspace_bytes), no zeroing needed but for its
  *                status word (first 256 bytes; read with moe_read_device_error)
- * Only T, d_model and n_experts of dims matter. Precision: fp32 products and sums (large batches:
- * on tensor cores, every fp32 operand as three bf16 terms). Deterministic for a given device. */
+ * Only T, d_model and n_experts of dims matter. Precision: fp32 products and sums. Large batches
+ * run on tensor cores, where an fp32 operand is a sum of 16-bit terms (22 bits of it or more) and
+ * sums are fp32: within 1e-6 of the exact result in norm. Deterministic for a given device. */
 moe_status moe_router_backward_workspace_bytes(const moe_dims* dims, size_t* bytes);
 moe_status moe_router_backward(const moe_dims* dims, const uint16_t* x, const float* w_router,
                                const float* d_logits, float* d_x, float* d_w_router,
@@ -409,7 +411,7 @@ moe_status moe_grad_norm(const moe_grad_tensor* tensors, int32_t n, float max_no
  *                value is rounded up with the probability of what is cut off; a nonzero v keeps a
  *                nonzero code; a block whose largest magnitude is below 2^-96 becomes zeros. This
  *                step's update uses the moments before that rounding. All zeros to begin with
- *   m_scale, v_scale  [ceil(numel / MOE_ADAMW_BLOCK)] fp32, state_bits 8 only */
+ *   m_scale, v_scale  [ceil(numel / MOE_ADAMW_BLOCK)] fp32 (4-byte aligned), state_bits 8 only */
 typedef struct {
   void* param;
   float* master;
@@ -426,7 +428,7 @@ typedef struct {
 } moe_adamw_tensor;
 
 typedef struct {
-  double lr, beta1, beta2, eps; /* 0 <= beta < 1, eps > 0 */
+  double lr, beta1, beta2, eps; /* 0 <= beta < 1, eps > 0 as an fp32 number */
   int32_t step;                 /* t of the bias corrections, 1 in the first step */
   uint32_t seed;                /* of the stochastic roundings */
   const int32_t* step_dev;      /* device int32 or NULL: t, in place of step, read when the kernel
@@ -439,7 +441,7 @@ typedef struct {
 /* One AdamW step (decoupled weight decay) over n tensors at once:
  *   g' = g grad_scale,  m' = beta1 m + (1 - beta1) g',  v' = beta2 v + (1 - beta2) g'^2,
  *   p' = p (1 - lr wd) - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
- * in fp32. The random bits of a rounding depend on seed, t, the tensor's place in the list and
+ * in fp32, each operation rounded by itself, in this order. The random bits of a rounding depend on seed, t, the tensor's place in the list and
  * the element, so equal calls give equal results. `tensors` and `config` are host memory, read
  * during the call; a graph that captures the call keeps the pointers that they held. Up to 384
  * tensors take one launch. No workspace. */

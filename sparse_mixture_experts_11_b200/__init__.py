@@ -505,10 +505,12 @@ def _one_device(names: str, *tensors) -> None:
 def balance_loss(dims: Dims, logits, topk_idx, token_mask, counts, n_tokens, prob_mean, loss,
                  d_logits, ws, alpha: float = 1e-2, z_coef: float = 0.0, d_loss=None,
                  stream=None) -> None:
-    """Balance loss and router z-loss over the tokens whose token_mask (uint8 or None) is not 0,
+    """Balance loss and router z-loss over the tokens whose token_mask (uint8, bool or None) is not 0,
     per-expert counts, and the gradient of the logits (d_logits may be None). loss [3] receives
     balance + z, balance, z; d_loss, a scalar tensor or None (1), is the total's gradient."""
     T, N, k = dims.T, dims.n_experts, dims.top_k
+    if token_mask is not None and token_mask.dtype is torch.bool:
+        token_mask = token_mask.view(torch.uint8)
     _one_device("logits topk_idx token_mask counts n_tokens prob_mean loss d_logits ws d_loss", logits,
                 topk_idx, token_mask, counts, n_tokens, prob_mean, loss, d_logits, ws, d_loss)
     _check(_lib.moe_balance_loss(

@@ -52,6 +52,8 @@ inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 moe_status check_dims(const moe_dims* d) {
@@ -759,7 +761,7 @@ moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n,
   if (n < 0 || (n > 0 && tensors == nullptr) || config == nullptr) return MOE_ERR_INVALID;
   const moe_adamw_config& c = *config;
   if (!isfinite(c.lr) || !(c.beta1 >= 0.0 && c.beta1 < 1.0) || !(c.beta2 >= 0.0 && c.beta2 < 1.0) ||
-      !(c.eps > 0.0) || !isfinite(c.eps))
+      !(static_cast<float>(c.eps) > 0.f) || !isfinite(static_cast<float>(c.eps)))
     return MOE_ERR_INVALID;
   if (c.step_dev == nullptr && c.step < 1) return MOE_ERR_INVALID;
   bool any = false;
@@ -776,7 +778,7 @@ moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n,
     if (!t.param || !t.grad || !t.m || !t.v) return MOE_ERR_INVALID;
     if (t.state_bits == 8 && (!t.m_scale || !t.v_scale)) return MOE_ERR_INVALID;
     if (!aligned16(t.param) || !aligned16(t.master) || !aligned16(t.grad) || !aligned16(t.m) ||
-        !aligned16(t.v) || !aligned16(t.m_scale) || !aligned16(t.v_scale))
+        !aligned16(t.v) || !aligned4(t.m_scale) || !aligned4(t.v_scale))
       return MOE_ERR_UNSUPPORTED;
   }
   if (!any) return MOE_OK;

@@ -61,9 +61,9 @@ TokenShape token_shape(int N) {
 }
 
 // CTAs of pass 2: one an SM, fewer when the tokens do not fill them.
-int balance_ctas(int T, int N, int most) {
+int balance_ctas(int64_t T, int N, int most) {
   const int per_cta = kBalWarps * (32 / token_shape(N).g);
-  return std::max(1, std::min((T + per_cta - 1) / per_cta, most));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((T + per_cta - 1) / per_cta, most)));
 }
 // floats of a CTA's row: N probabilities rounded up to four, then sum of lse^2 and padding
 __host__ __device__ constexpr int row_floats(int N) { return (N + 3) / 4 * 4 + 4; }
@@ -352,7 +352,7 @@ size_t balance_scratch_bytes(int64_t T, int N) {
   if (T == 0) return 0;
   const size_t rows = static_cast<size_t>(count_plan(T).rows) * (N + 1) * sizeof(int32_t);
   return (rows + 15) / 16 * 16 +
-         static_cast<size_t>(balance_ctas(static_cast<int>(T), N, kBalanceMaxCtas)) * row_floats(N) *
+         static_cast<size_t>(balance_ctas(T, N, kBalanceMaxCtas)) * row_floats(N) *
              sizeof(float);
 }
 

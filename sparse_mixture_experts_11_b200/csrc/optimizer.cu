@@ -22,13 +22,14 @@
 // probability of the part cut off keeps its expectation. A nonzero r keeps a nonzero code, so
 // that no m is divided by eps alone. The random bits are a function of (seed, step, place of the
 // tensor in the list, element), so a step is reproducible.
-// Where a value lies next to a border of the codes, its last bit decides between codes 6 to 12 %
-// apart, and a block's next scale can hang on one code. So with 8 bits m', v' and sqrt(v'), and the
-// update of a bf16 parameter without a master copy, are computed in the order of the
-// formulas, every operation rounded by itself (no fused multiply-add; square root, quotient and
-// reciprocal to nearest): any fp32 implementation of these lines has the same results, bit by bit.
 // A bf16 parameter without an fp32 master copy is rounded the same way: most updates are below
 // half its spacing.
+//
+// Where a value lies next to a border of the codes, its last bit decides between codes 6 to 12 %
+// apart, and a block's next scale can hang on one code. So every fp32 operation is rounded by
+// itself, in the order of the formulas (no fused multiply-add; square root, quotient and
+// reciprocal to nearest): any fp32 implementation of these lines has the same results, bit by bit.
+// 537M elements with masters take 2365 us so, 2305 with approximate roots and quotients.
 #include <math.h>
 
 #include <algorithm>
@@ -213,18 +214,6 @@ struct StepScalars {  // what every element needs; omb: 1 - beta
   float lr_wd1, step_size, inv_sqrt_bc2, eps;  // 1 - lr wd, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
 };
 
-// One special-function operation each, within 2^-23; with fp32 moments a v below 2^-126 has root zero.
-__device__ __forceinline__ float sqrt_approx(float x) {
-  float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp_approx(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // Two fp32 operations in one instruction (sm_100): the kernel is bound by instruction issue where
 // the moments are 8 bits wide, and half of its instructions are fp32 arithmetic.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -242,14 +231,6 @@ __device__ __forceinline__ float2 mul2_rn(float2 a, float b) {
 }
 __device__ __forceinline__ float2 add2_rn(float2 a, float2 b) {
   return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
@@ -393,33 +374,20 @@ __device__ __forceinline__ void adam_block(const AdamEntry& t, const StepScalars
   }
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
+    // every operation rounded by itself, in the order of the formulas: see the top of the file
     const float2 gv = mul2(g[q], both(s.gs));
-    if (BITS8 || PARAMS == kAlone) {
-      // every operation rounded by itself, in the order of the formulas: see the top of the file
-      if (BITS8) {
-        m[q] = mul2(m[q], both(w.ms));
-        v[q] = mul2(v[q], both(w.vs));
-        v[q] = mul2(v[q], v[q]);
-      }
-      m[q] = add2_rn(mul2_rn(m[q], s.b1), mul2_rn(gv, s.omb1));
-      const float2 gg = mul2(gv, both(s.omb2));
-      v[q] = add2_rn(mul2_rn(v[q], s.b2), make_float2(__fmul_rn(gg.x, gv.x), __fmul_rn(gg.y, gv.y)));
-      r[q] = make_float2(__fsqrt_rn(v[q].x), __fsqrt_rn(v[q].y));
-    } else {
-      m[q] = fma2(m[q], both(s.b1), mul2(gv, both(s.omb1)));
-      v[q] = fma2(v[q], both(s.b2), mul2(mul2(gv, both(s.omb2)), gv));
-      r[q] = make_float2(sqrt_approx(v[q].x), sqrt_approx(v[q].y));
+    if (BITS8) {
+      m[q] = mul2(m[q], both(w.ms));
+      v[q] = mul2(v[q], both(w.vs));
+      v[q] = mul2(v[q], v[q]);
     }
-    if (PARAMS == kAlone) {
-      const float2 num = mul2(both(s.step_size), m[q]), keep = mul2_rn(p[q], s.lr_wd1);
-      const float2 den = add2_rn(mul2_rn(r[q], s.inv_sqrt_bc2), both(s.eps));
-      p[q] = make_float2(__fsub_rn(keep.x, __fdiv_rn(num.x, den.x)), __fsub_rn(keep.y, __fdiv_rn(num.y, den.y)));
-    } else {
-      const float2 den = fma2(r[q], both(s.inv_sqrt_bc2), both(s.eps));
-      const float2 upd = mul2(mul2(m[q], both(-s.step_size)),
-                              make_float2(rcp_approx(den.x), rcp_approx(den.y)));
-      p[q] = fma2(p[q], both(s.lr_wd1), upd);
-    }
+    m[q] = add2_rn(mul2_rn(m[q], s.b1), mul2_rn(gv, s.omb1));
+    const float2 gg = mul2(gv, both(s.omb2));
+    v[q] = add2_rn(mul2_rn(v[q], s.b2), make_float2(__fmul_rn(gg.x, gv.x), __fmul_rn(gg.y, gv.y)));
+    r[q] = make_float2(__fsqrt_rn(v[q].x), __fsqrt_rn(v[q].y));
+    const float2 num = mul2(both(s.step_size), m[q]), keep = mul2_rn(p[q], s.lr_wd1);
+    const float2 den = add2_rn(mul2_rn(r[q], s.inv_sqrt_bc2), both(s.eps));
+    p[q] = make_float2(__fsub_rn(keep.x, __fdiv_rn(num.x, den.x)), __fsub_rn(keep.y, __fdiv_rn(num.y, den.y)));
   }
   uint32_t h[4];
   if (BITS8 || PARAMS == kAlone) {

@@ -263,6 +263,43 @@ def test_router_backward_zero_gradient():
     assert all(torch.count_nonzero(t) == 0 for t in (dx, dw, db))
 
 
+@pytest.mark.parametrize("N", [20, 50, 200])
+def test_router_backward_timeout_is_reported(N):
+    """With a wait limit far too short the tensor-core kernels may stop early: they drain what they
+    issued and say so, and the context and the next call are as before. An attempt to wait suspends
+    the thread for a while and the limit is looked at after a failed one, so a kernel whose every wait
+    ends within the attempt finishes, with the right results and no error."""
+    T, d = 4096, 2048
+    dims = moe.make_dims(T, d, N, 1, 64)
+    ws = moe.new_router_backward_workspace(dims)
+    x, w, g = randn(T, d).to(torch.bfloat16), randn(N, d), randn(T, N)
+    outs = [torch.zeros(s, device="cuda") for s in ((T, d), (N, d), (N,))]
+    moe.debug_set_wait_timeout_ns(1)
+    try:
+        moe.router_backward(dims, x, w, g, *outs, ws)
+        torch.cuda.synchronize()
+    finally:
+        moe.debug_set_wait_timeout_ns(0)
+    old = dict(d_x=0.0, d_w_router=0.0, d_logit_bias=0.0)
+    status = moe.read_device_error(ws)
+    assert status in (moe.OK, moe.ERR_TIMEOUT)
+    if status == moe.OK:
+        check_router(T, d, N, x, w, g, dict(zip(old, outs)), old, tuple(old))
+    moe.router_backward(dims, x, w, g, *outs, ws)
+    torch.cuda.synchronize()
+    assert moe.read_device_error(ws) == moe.OK
+    check_router(T, d, N, x, w, g, dict(zip(old, outs)), old, tuple(old))
+
+
+def test_balance_loss_bool_mask():
+    L = randn(100, 8, seed=1)
+    idx = L.topk(2, 1).indices.to(torch.int32)
+    mask = torch.rand(100, generator=gen(2), device="cuda") < 0.5
+    a, b = run_balance(L, idx, mask), run_balance(L, idx, mask.to(torch.uint8))
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+
+
 # ---------------------------------------------------------------- gradient norm
 @pytest.mark.parametrize("sizes", [[], [0], [1], [5, 0, 3], [128] * 300, [1 << 20, 7, 12345], [3] * 2500,
                                    [33_000_001]])
@@ -463,11 +500,10 @@ def test_adamw_step_and_rate_on_the_device_replayed():
         assert float((x != y).float().mean()) < 5e-3 and torch.allclose(x, y, rtol=0.13, atol=2e-4), k
 
 
-@pytest.mark.parametrize("kind", [k for k in KINDS if k[2] == 8 or k[0] == "bf16"],
-                         ids=lambda k: f"{k[0]}-{str(k[1])[6:]}-{k[2]}")
-def test_adamw_rounded_states_bit_by_bit(kind):
-    """Where codes are kept, every fp32 operation is rounded by itself in the order of the formulas: the
-    same lines in fp32 tensor operations give the same bits, over several steps."""
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: f"{k[0]}-{str(k[1])[6:]}-{k[2]}")
+def test_adamw_bit_by_bit(kind):
+    """Every fp32 operation is rounded by itself in the order of the formulas: the same lines in fp32
+    tensor operations give the same bits, over several steps."""
     n, lr, b1, b2, eps, wd, seed = 128 * 20000, 3e-4, 0.9, 0.999, 1e-8, 0.1, 11
     t = make_tensor(n, kind, seed=21)
     t["grad"] = t["grad"].float().to(kind[1])
@@ -515,10 +551,7 @@ def test_adamw_rounded_states_bit_by_bit(kind):
             w = ((w.view(torch.int32) + up) & -65536).view(torch.float32)
             assert torch.equal(t["param"].float(), w)
         else:
-            # the fp32 parameter rounds twice a step on either side (4 u of it together) and its update,
-            # below 3 lr here, has approximate square roots and quotients (32 u of it): three steps
-            torch.testing.assert_close(t["master"] if kind[0] == "master" else t["param"], w, rtol=3 * 4 * U,
-                                       atol=3 * 32 * U * 3 * lr)
+            assert torch.equal(t["master"] if kind[0] == "master" else t["param"], w)
 
 
 def test_adamw_moments_in_8_bits_keep_their_expectation():
@@ -648,8 +681,8 @@ def test_training_step_end_to_end(T, d, N, k, F, act):
             assert np.abs(got - o["param"]).max() <= 1e-3 * 1e-5 + 4 * U * np.abs(got).max()
 
 
-def test_training_step_replayed_on_a_side_stream_equals_calls():
-    shape = (300, 128, 8, 2, 64, "swiglu")
+@pytest.mark.parametrize("shape", [(300, 128, 8, 2, 64, "swiglu"), (2100, 1024, 64, 2, 64, "gelu")])
+def test_training_step_replayed_on_a_side_stream_equals_calls(shape):
     go, *_, b1, p1, s1, _, _, _ = train_step(*shape, seed=3)
     go()
     go()

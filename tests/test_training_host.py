@@ -182,6 +182,8 @@ def _adam(n=None, config=None, **kw):
     (dict(weight_decay=float("nan")), moe.ERR_INVALID), (dict(grad=20), moe.ERR_UNSUPPORTED),
     (dict(m=17, state_bits=8, m_scale=16, v_scale=16), moe.ERR_UNSUPPORTED),
     (dict(master=8, param_dtype=1), moe.ERR_UNSUPPORTED),
+    (dict(state_bits=8, m_scale=18, v_scale=16), moe.ERR_UNSUPPORTED),
+    (dict(config=dict(eps=1e-60)), moe.ERR_INVALID), (dict(config=dict(eps=1e60)), moe.ERR_INVALID),
     (dict(config=dict(step=0)), moe.ERR_INVALID), (dict(config=dict(eps=0.0)), moe.ERR_INVALID),
     (dict(config=dict(beta1=1.0)), moe.ERR_INVALID), (dict(config=dict(beta2=-0.1)), moe.ERR_INVALID),
     (dict(config=dict(lr=float("inf"))), moe.ERR_INVALID), (dict(config=dict(eps=float("nan"))), moe.ERR_INVALID),
