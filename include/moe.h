@@ -443,8 +443,8 @@ typedef struct {
  *   p' = p (1 - lr wd) - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
  * in fp32, each operation rounded by itself, in this order. The random bits of a rounding depend on seed, t, the tensor's place in the list and
  * the element, so equal calls give equal results. `tensors` and `config` are host memory, read
- * during the call; a graph that captures the call keeps the pointers that they held. Up to 384
- * tensors take one launch. No workspace. */
+ * during the call; a graph that captures the call keeps the pointers that they held. A launch
+ * takes up to 384 tensors, and large lists a launch for each kind of moments. No workspace. */
 moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n,
                           const moe_adamw_config* config, void* stream);
 

@@ -44,6 +44,9 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kOptThreads = 256;
 constexpr int kOptWarps = kOptThreads / 32;
+// Mixed lists up to here (in tiles) take one launch for both kinds of moments. Device time of one
+// launch and of two, us: 384 tiles 5.1, 9.8; 1930 tiles 21.0, 25.1; 6146 tiles 51.9, 54.2; 24584 tiles 224.8, 223.2.
+constexpr int64_t kBothTiles = 8192;
 constexpr int kTileBlocks = 2 * kOptWarps;  // a tile: two blocks for each warp of a CTA
 constexpr int kQBlock = MOE_ADAMW_BLOCK;  // elements of a block: one warp, four a lane
 static_assert(kQBlock == 128, "a warp takes one block, four elements a lane");
@@ -191,7 +194,7 @@ struct AdamEntry {
   int32_t chunk0;
   int32_t index;  // place in the caller's list
   float weight_decay;
-  uint8_t params, grad_bf16;
+  uint8_t params, grad_bf16, bits8;
 };
 struct AdamScalars {
   float b1, omb1, b2, omb2, eps;  // omb: 1 - beta
@@ -487,10 +490,12 @@ __device__ __forceinline__ void adam_run(const AdamEntry& t, const StepScalars& 
   }
 }
 
-// BITS8: the table holds tensors with 8-bit moments, else with fp32 ones (two kernels: the
-// conversions of the one would cost the other its registers).
-template <bool BITS8, int CAP>
-__global__ void __launch_bounds__(kOptThreads, BITS8 ? 4 : 3)
+// KIND: the table holds tensors with fp32 moments, with 8-bit ones, or both. Large lists take a
+// kernel for each (the conversions of the one would cost the other its registers), small mixed
+// lists one launch for both.
+enum { kMoments32 = 0, kMoments8 = 1, kBoth = 2 };
+template <int KIND, int CAP>
+__global__ void __launch_bounds__(kOptThreads, KIND == kMoments8 ? 4 : 3)
     adamw_kernel(const __grid_constant__ AdamTable<CAP> tab, const AdamScalars sc) {
   __shared__ float s_bc[2];
   pdl_trigger();
@@ -526,7 +531,7 @@ __global__ void __launch_bounds__(kOptThreads, BITS8 ? 4 : 3)
         mix32(mix32(static_cast<uint32_t>(t.index) * 0x632BE5ABu + sc.seed) +
               static_cast<uint32_t>(step) * 0x9E3779B1u);
     // uniform over the CTA
-    if (BITS8) {
+    if (KIND == kMoments8 || (KIND == kBoth && t.bits8)) {
       switch (t.params * 2 + t.grad_bf16) {
         case 0: adam_run<kFp32, false, true>(t, s, tile, n, key); break;
         case 1: adam_run<kFp32, true, true>(t, s, tile, n, key); break;
@@ -553,15 +558,23 @@ constexpr int kAdamTable = 384, kAdamTableShort = 32;
 static_assert(sizeof(AdamTable<kAdamTable>) + sizeof(AdamScalars) <= 32764, "kernel parameters");
 static_assert(sizeof(NormTable<kNormTable>) + 64 <= 32764, "kernel parameters");
 
-// The tensors of one kind (8-bit or fp32 moments) of the list, CAP a launch.
-template <bool BITS8, int CAP>
-cudaError_t launch_adamw_kind(const moe_adamw_tensor* tensors, int n, const AdamScalars& sc, int sms,
-                              cudaStream_t s) {
-  int64_t total = 0;  // tiles
+template <int KIND>
+bool of_kind(const moe_adamw_tensor& t) {
+  return t.numel > 0 && (KIND == kBoth || (t.state_bits == 8) == (KIND == kMoments8));
+}
+
+template <int KIND>
+int64_t tiles_of(const moe_adamw_tensor* tensors, int n) {
+  int64_t total = 0;
   for (int i = 0; i < n; ++i)
-    if (tensors[i].numel > 0 && (tensors[i].state_bits == 8) == BITS8)
-      total += (tensors[i].numel - 1) / (kTileBlocks * kQBlock) + 1;
-  if (total == 0) return cudaSuccess;
+    if (of_kind<KIND>(tensors[i])) total += (tensors[i].numel - 1) / (kTileBlocks * kQBlock) + 1;
+  return total;
+}
+
+// The tensors of a kind, CAP a launch.
+template <int KIND, int CAP>
+cudaError_t launch_adamw_kind(const moe_adamw_tensor* tensors, int n, int64_t total, const AdamScalars& sc, int sms,
+                              cudaStream_t s) {
   // fp32 moments: a CTA a tile, in the tensor's order. What bounds the kernel is how well the
   // memory streams, and CTAs that start in order keep all SMs within a few pages of each other
   // (537M elements with masters: 2308 us; persistent CTAs on chunks of 16 tiles, 2550 us).
@@ -569,7 +582,7 @@ cudaError_t launch_adamw_kind(const moe_adamw_tensor* tensors, int n, const Adam
   // bound, and a CTA's start is half of a tile's (1514 us; a CTA a tile, 1691 us).
   const int64_t resident = static_cast<int64_t>(sms) * 4;
   int chunk_tiles = 1;
-  while (BITS8 && chunk_tiles < 32 && total / chunk_tiles > 8 * resident) chunk_tiles *= 2;
+  while (KIND == kMoments8 && chunk_tiles < 32 && total / chunk_tiles > 8 * resident) chunk_tiles *= 2;
   AdamTable<CAP> tab;
   for (int i = 0; i < n;) {
     tab.n = 0;
@@ -577,7 +590,7 @@ cudaError_t launch_adamw_kind(const moe_adamw_tensor* tensors, int n, const Adam
     int64_t chunks = 0;
     for (; i < n && tab.n < CAP; ++i) {
       const moe_adamw_tensor& in = tensors[i];
-      if (in.numel == 0 || (in.state_bits == 8) != BITS8) continue;
+      if (!of_kind<KIND>(in)) continue;
       const int64_t c = ((in.numel - 1) / (kTileBlocks * kQBlock) + chunk_tiles) / chunk_tiles;
       if (chunks + c > INT32_MAX) return cudaErrorInvalidValue;
       AdamEntry& t = tab.e[tab.n++];
@@ -594,15 +607,28 @@ cudaError_t launch_adamw_kind(const moe_adamw_tensor* tensors, int n, const Adam
       t.weight_decay = in.weight_decay;
       t.params = in.param_dtype == MOE_DTYPE_F32 ? kFp32 : in.master != nullptr ? kMaster : kAlone;
       t.grad_bf16 = in.grad_dtype == MOE_DTYPE_BF16;
+      t.bits8 = in.state_bits == 8;
       chunks += c;
     }
     if (chunks == 0) break;
     tab.chunks = static_cast<int>(chunks);
-    const int grid = static_cast<int>(BITS8 ? std::min<int64_t>(chunks, resident) : chunks);
-    const cudaError_t e = launch_pdl(adamw_kernel<BITS8, CAP>, dim3(grid), dim3(kOptThreads), 0, s, tab, sc);
+    const int grid = static_cast<int>(KIND == kMoments8 ? std::min<int64_t>(chunks, resident) : chunks);
+    const cudaError_t e = launch_pdl(adamw_kernel<KIND, CAP>, dim3(grid), dim3(kOptThreads), 0, s, tab, sc);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+template <int CAP>
+cudaError_t launch_adamw_tables(const moe_adamw_tensor* tensors, int n, const AdamScalars& sc, int sms,
+                                cudaStream_t s) {
+  const int64_t t32 = tiles_of<kMoments32>(tensors, n), t8 = tiles_of<kMoments8>(tensors, n);
+  if (t32 > 0 && t8 > 0 && t32 + t8 <= kBothTiles)
+    return launch_adamw_kind<kBoth, CAP>(tensors, n, t32 + t8, sc, sms, s);
+  cudaError_t e = cudaSuccess;
+  if (t32 > 0) e = launch_adamw_kind<kMoments32, CAP>(tensors, n, t32, sc, sms, s);
+  if (e == cudaSuccess && t8 > 0) e = launch_adamw_kind<kMoments8, CAP>(tensors, n, t8, sc, sms, s);
+  return e;
 }
 
 template <int CAP>
@@ -681,12 +707,8 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int n, const moe_adamw
   sc.step_dev = cfg.step_dev;
   sc.lr_dev = cfg.lr_dev;
   sc.grad_scale = cfg.grad_scale;
-  if (n <= kAdamTableShort) {
-    e = launch_adamw_kind<false, kAdamTableShort>(tensors, n, sc, di.sm_count, s);
-    return e != cudaSuccess ? e : launch_adamw_kind<true, kAdamTableShort>(tensors, n, sc, di.sm_count, s);
-  }
-  e = launch_adamw_kind<false, kAdamTable>(tensors, n, sc, di.sm_count, s);
-  return e != cudaSuccess ? e : launch_adamw_kind<true, kAdamTable>(tensors, n, sc, di.sm_count, s);
+  return n <= kAdamTableShort ? launch_adamw_tables<kAdamTableShort>(tensors, n, sc, di.sm_count, s)
+                              : launch_adamw_tables<kAdamTable>(tensors, n, sc, di.sm_count, s);
 }
 
 }  // namespace moe

@@ -334,11 +334,14 @@ __device__ __forceinline__ uint16_t fp16_term(float& v) {
   v -= __half2float(h);
   return __half_as_ushort(h);
 }
-// e with 2^(e-1) <= |v| < 2^e; 0 for zero
+// e with |v| < 2^e, and 2^(e-1) <= |v| but for subnormal numbers and zero (-125).
 __device__ __forceinline__ int exponent_of(float v) {
-  int e = 0;
-  frexpf(v, &e);
-  return e;
+  return max(static_cast<int>(__float_as_uint(v) >> 23 & 0xffu), 1) - 126;
+}
+// v 2^s for a result below 2^15, in two factors: exact where the result is a normal number.
+__device__ __forceinline__ float scale_by(float v, int s) {
+  const int s1 = max(-126, min(127, s)), s2 = max(-126, min(127, s - s1));
+  return v * __uint_as_float(static_cast<uint32_t>(s1 + 127) << 23) * __uint_as_float(static_cast<uint32_t>(s2 + 127) << 23);
 }
 
 // CTA n: row n of W_r as two fp16 terms [2][N][d], scaled by 2^(14 - b_n), and b_n.
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(kThreads) split_w_kernel(const float* __restri
 #pragma unroll 4
   for (int i = threadIdx.x; i < d / 4; i += kThreads) {
     const float4 v4 = __ldg(src + i);
-    float v[4] = {scalbnf(v4.x, 14 - b), scalbnf(v4.y, 14 - b), scalbnf(v4.z, 14 - b), scalbnf(v4.w, 14 - b)};
+    float v[4] = {scale_by(v4.x, 14 - b), scale_by(v4.y, 14 - b), scale_by(v4.z, 14 - b), scale_by(v4.w, 14 - b)};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       uint16_t t[4];
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(kThreads) split_dl_kernel(
       for (int j = 0; j < 4; ++j) {
         const int n = j * 64 + lane * 2;
         if (n >= np) break;
-        float x = scalbnf(v[2 * j], 14 + b[2 * j] - top), y = scalbnf(v[2 * j + 1], 14 + b[2 * j + 1] - top);
+        float x = scale_by(v[2 * j], 14 + b[2 * j] - top), y = scale_by(v[2 * j + 1], 14 + b[2 * j + 1] - top);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const uint32_t lo = fp16_term(x), hi = fp16_term(y);
