@@ -36,7 +36,7 @@ Plan make_plan(int64_t T, int N, int d) {
   p.w_cols = (d + kWCols - 1) / kWCols;
   p.w_experts = (N + kWExperts - 1) / kWExperts;
   const int64_t tiles = static_cast<int64_t>(p.w_cols) * p.w_experts;
-  const int64_t most = (T + 4 * kWTokens - 1) / (4 * kWTokens);  // ranges of at least 128 tokens
+  const int64_t most = (T + 2 * kWTokens - 1) / (2 * kWTokens);  // ranges of at least 64 tokens
   const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>({most, 2 * 148 / tiles, 64}));
   p.chunk = (T + chunks - 1) / chunks;
   p.chunks = T > 0 ? static_cast<int>((T + p.chunk - 1) / p.chunk) : 0;
@@ -67,20 +67,41 @@ __device__ __forceinline__ void w_tile(const Params& a, uint32_t (*s_x)[kWCols /
   const int cp = threadIdx.x & 63, eg = threadIdx.x >> 6;  // column pair, group of 4 experts
   float acc[4][2] = {};
   float b = 0.f;
-  for (int64_t tb = t0; tb < t1; tb += kWTokens) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kWTokens * (kWCols / 2); i += kThreads) {
-      const int64_t t = tb + i / (kWCols / 2);
-      const int c = c0 + i % (kWCols / 2) * 2;
-      s_x[i / (kWCols / 2)][i % (kWCols / 2)] =
-          t < t1 && c < a.d ? *reinterpret_cast<const uint32_t*>(a.x + t * a.d + c) : 0u;
+  // the next tile's loads are under way while a tile is used: 16 bytes of x and of dL a thread
+  constexpr int kXLoads = kWTokens * kWCols / 8 / kThreads, kDlLoads = kWTokens * kWExperts / kThreads;
+  uint4 nx[kXLoads];
+  float nd[kDlLoads];
+  auto fetch = [&](int64_t tb) {
+#pragma unroll
+    for (int k = 0; k < kXLoads; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      const int64_t t = tb + i / (kWCols / 8);
+      const int c = c0 + i % (kWCols / 8) * 8;
+      nx[k] = t < t1 && c < a.d ? __ldg(reinterpret_cast<const uint4*>(a.x + t * a.d + c)) : make_uint4(0u, 0u, 0u, 0u);
     }
-    for (int i = threadIdx.x; i < kWTokens * kWExperts; i += kThreads) {
+#pragma unroll
+    for (int k = 0; k < kDlLoads; ++k) {
+      const int i = threadIdx.x + k * kThreads;
       const int64_t t = tb + i / kWExperts;
       const int n = n0 + i % kWExperts;
-      s_dl[i / kWExperts][i % kWExperts] = t < t1 && n < a.N ? a.dl[t * a.N + n] : 0.f;
+      nd[k] = t < t1 && n < a.N ? __ldg(a.dl + t * a.N + n) : 0.f;
+    }
+  };
+  fetch(t0);
+  for (int64_t tb = t0; tb < t1; tb += kWTokens) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kXLoads; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      *reinterpret_cast<uint4*>(&s_x[i / (kWCols / 8)][i % (kWCols / 8) * 4]) = nx[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kDlLoads; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      s_dl[i / kWExperts][i % kWExperts] = nd[k];
     }
     __syncthreads();
+    fetch(tb + kWTokens);
 #pragma unroll 8
     for (int u = 0; u < kWTokens; ++u) {
       const uint32_t xv = s_x[u][cp];
@@ -137,7 +158,7 @@ __device__ __forceinline__ void x_tile(const Params& a, float (*s_dl)[kXExperts]
     __syncthreads();
     const int n1 = min(kXExperts, a.N - nb);
     if (c < a.d) {
-#pragma unroll 4
+#pragma unroll 8
       for (int n = 0; n < n1; ++n) {
         const float4 w = __ldg(reinterpret_cast<const float4*>(a.w + static_cast<int64_t>(nb + n) * a.d + c));
 #pragma unroll
@@ -169,7 +190,7 @@ __device__ __forceinline__ void x_tile(const Params& a, float (*s_dl)[kXExperts]
 }
 
 __global__ void __launch_bounds__(kThreads) router_backward_kernel(const Params a) {
-  __shared__ uint32_t s_x[kWTokens][kWCols / 2];
+  __shared__ __align__(16) uint32_t s_x[kWTokens][kWCols / 2];
   __shared__ float s_w[kWTokens][kWExperts];
   __shared__ float s_dl[kXTokens][kXExperts];
   pdl_trigger();
@@ -178,11 +199,14 @@ __global__ void __launch_bounds__(kThreads) router_backward_kernel(const Params 
   else x_tile(a, s_dl);
 }
 
-// The token ranges' partial sums, added in order (CTAs [0, w_ctas): four elements of dW_r a thread);
-// the bias gradient's by a warp an expert, 32 strided sums and their tree.
+// The token ranges' partial sums. CTAs [0, w_ctas): 64 float4s of dW_r each, four threads a float4
+// over a quarter of the ranges, whose sums are added in order; the bias gradient's by a warp an
+// expert, 32 strided sums and their tree.
+constexpr int kSumItems = 64;
 __global__ void __launch_bounds__(256) router_backward_sum_kernel(
     const float* __restrict__ part_w, const float* __restrict__ part_b, float* __restrict__ d_w,
     float* __restrict__ d_b, int chunks, int b_parts, int N, int d, int accumulate, int w_ctas) {
+  __shared__ float4 s_part[4][kSumItems];
   pdl_trigger();
   pdl_wait();
   if (static_cast<int>(blockIdx.x) >= w_ctas) {
@@ -197,12 +221,26 @@ __global__ void __launch_bounds__(256) router_backward_sum_kernel(
     return;
   }
   const int64_t items = static_cast<int64_t>(N) * d / 4;
-  const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-  if (i >= items) return;
+  const int quarter = threadIdx.x / kSumItems, j = threadIdx.x % kSumItems;
+  const int64_t i = blockIdx.x * static_cast<int64_t>(kSumItems) + j;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = 0; c < chunks; ++c) {
-    const float4 v = reinterpret_cast<const float4*>(part_w)[c * items + i];
+  if (i < items) {
+    const int c1 = chunks * (quarter + 1) / 4;
+#pragma unroll 8
+    for (int c = chunks * quarter / 4; c < c1; ++c) {
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(part_w) + c * items + i);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+  }
+  s_part[quarter][j] = s;
+  __syncthreads();
+  if (quarter != 0 || i >= items) return;
+#pragma unroll
+  for (int q = 1; q < 4; ++q) {
+    const float4 v = s_part[q][j];
     s.x += v.x;
     s.y += v.y;
     s.z += v.z;
@@ -222,7 +260,7 @@ __global__ void __launch_bounds__(256) router_backward_sum_kernel(
 cudaError_t launch_sum(const float* part_w, const float* part_b, const RouterBackwardArgs& a, int chunks,
                        int b_parts, cudaStream_t s) {
   const int64_t items = static_cast<int64_t>(a.N) * a.d / 4;
-  const int w_ctas = a.d_w_router != nullptr ? static_cast<int>((items + 255) / 256) : 0;
+  const int w_ctas = a.d_w_router != nullptr ? static_cast<int>((items + kSumItems - 1) / kSumItems) : 0;
   const int b_ctas = a.d_logit_bias != nullptr ? (a.N + 7) / 8 : 0;
   return launch_pdl(router_backward_sum_kernel, dim3(w_ctas + b_ctas), dim3(256), 0, s, part_w, part_b,
                     a.d_w_router, a.d_logit_bias, chunks, b_parts, a.N, a.d, a.accumulate, w_ctas);
@@ -844,9 +882,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // Tensor cores where the products are worth the five launches, from T N d = 2^26 on. Device time
-// of the two paths, CUDA cores first, us, at (T, d, N): (256, 1024, 64) 12.0, 20.7; (512, 2880, 32) 19.1,
-// 20.7; (1024, 1024, 64) 20.1, 21.7; (64, 4096, 256) 37.0, 30.7; (4096, 512, 64) 36.6, 23.9;
-// (4096, 2880, 32) 94, 33; (1024, 4096, 128) 126, 29. Below 64 tokens a row block of the MMA is half empty.
+// of the two paths, CUDA cores first, us, at (T, d, N): (256, 1024, 64) 12.1, 18.4; (512, 2880, 32) 15.2,
+// 18.8; (1024, 1024, 64) 18.1, 20.5; (64, 4096, 256) 26.4, 24.0; (4096, 512, 64) 30.4, 22.2;
+// (4096, 2880, 32) 70, 30; (1024, 4096, 128) 83, 26. Below 64 tokens a row block of the MMA is half empty.
 bool use_tensor_cores(int64_t T, int N, int d) { return T >= 64 && static_cast<double>(T) * N * d >= 67108864.0; }
 
 template <int GROUP>
