@@ -48,6 +48,7 @@ constexpr int kOptWarps = kOptThreads / 32;
 // launch and of two, us: 384 tiles 5.1, 9.8; 1930 tiles 21.0, 25.1; 6146 tiles 51.9, 54.2; 24584 tiles 224.8, 223.2.
 constexpr int64_t kBothTiles = 8192;
 constexpr int kTileBlocks = 2 * kOptWarps;  // a tile: two blocks for each warp of a CTA
+constexpr int64_t kMaxChunks = 1 << 30;  // of a launch: a kernel's chunk index plus its grid is an int
 constexpr int kQBlock = MOE_ADAMW_BLOCK;  // elements of a block: one warp, four a lane
 static_assert(kQBlock == 128, "a warp takes one block, four elements a lane");
 
@@ -577,9 +578,9 @@ cudaError_t launch_adamw_kind(const moe_adamw_tensor* tensors, int n, int64_t to
                               cudaStream_t s) {
   // fp32 moments: a CTA a tile, in the tensor's order. What bounds the kernel is how well the
   // memory streams, and CTAs that start in order keep all SMs within a few pages of each other
-  // (537M elements with masters: 2308 us; persistent CTAs on chunks of 16 tiles, 2550 us).
+  // (537M elements with masters: 2377 us; persistent CTAs on chunks of 16 tiles, 2696 us).
   // 8 bits: as many CTAs as are resident, on chunks that grow with the total: here instructions
-  // bound, and a CTA's start is half of a tile's (1514 us; a CTA a tile, 1691 us).
+  // bound, and a CTA's start is a part of a tile's (1770 us; a CTA a tile, 1911 us).
   const int64_t resident = static_cast<int64_t>(sms) * 4;
   int chunk_tiles = 1;
   while (KIND == kMoments8 && chunk_tiles < 32 && total / chunk_tiles > 8 * resident) chunk_tiles *= 2;
@@ -592,7 +593,7 @@ cudaError_t launch_adamw_kind(const moe_adamw_tensor* tensors, int n, int64_t to
       const moe_adamw_tensor& in = tensors[i];
       if (!of_kind<KIND>(in)) continue;
       const int64_t c = ((in.numel - 1) / (kTileBlocks * kQBlock) + chunk_tiles) / chunk_tiles;
-      if (chunks + c > INT32_MAX) return cudaErrorInvalidValue;
+      if (chunks + c > kMaxChunks) return cudaErrorInvalidValue;
       AdamEntry& t = tab.e[tab.n++];
       t.param = in.param;
       t.master = in.master;
@@ -654,7 +655,7 @@ cudaError_t launch_grad_norm_tables(const moe_grad_tensor* tensors, int n, float
     for (; i < n && tab.n < CAP; ++i) {
       if (tensors[i].numel == 0) continue;
       const int64_t c = (tensors[i].numel + chunk - 1) / chunk;
-      if (chunks + c > INT32_MAX) return cudaErrorInvalidValue;
+      if (chunks + c > kMaxChunks) return cudaErrorInvalidValue;
       NormEntry& t = tab.e[tab.n++];
       t.grad = tensors[i].grad;
       t.numel = tensors[i].numel;
