@@ -494,12 +494,30 @@ def backward_into(dims: Dims, x, w_router, w_gate_up, w_down, fwd_ws, d_out, d_x
 
 
 # ----------------------------------------------------------------------------- training
-def _one_device(names: str, *tensors) -> None:
-    """All tensors on the current device: the library launches there."""
-    here = torch.cuda.current_device()
-    for i, t in enumerate(tensors):
-        if t is not None and t.is_cuda and t.get_device() != here:
-            raise ValueError(f"{names.split()[i]} is on {t.device}, the current device is cuda:{here}")
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _arg(t, here: int, name: str, dtype, shape) -> int:
+    """Address of a tensor that must lie on the current device (the library launches there). One
+    short test where all is well: the smallest calls cost little more than this."""
+    if t is not None and t.get_device() == here and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    p = _ptr(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}") if p is not None else None
+
+
+def _opt(t, here: int, name: str, dtype, shape):
+    return None if t is None else _arg(t, here, name, dtype, shape)
+
+
+def _workspace(ws, here: int) -> tuple:
+    if ws is not None and ws.get_device() == here and ws.dtype is torch.uint8 and ws.is_contiguous():
+        return ws.data_ptr(), ws.numel()
+    return _arg(ws, here, "ws", torch.uint8, None if ws is None else tuple(ws.shape)), _nbytes(ws)
+
+
+def _stream_on(stream, here: int) -> int:
+    return _raw_stream(here) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def balance_loss(dims: Dims, logits, topk_idx, token_mask, counts, n_tokens, prob_mean, loss,
@@ -511,18 +529,15 @@ def balance_loss(dims: Dims, logits, topk_idx, token_mask, counts, n_tokens, pro
     T, N, k = dims.T, dims.n_experts, dims.top_k
     if token_mask is not None and token_mask.dtype is torch.bool:
         token_mask = token_mask.view(torch.uint8)
-    _one_device("logits topk_idx token_mask counts n_tokens prob_mean loss d_logits ws d_loss", logits,
-                topk_idx, token_mask, counts, n_tokens, prob_mean, loss, d_logits, ws, d_loss)
+    here, f32, i32 = _device(), torch.float32, torch.int32
+    wp, wn = _workspace(ws, here)
     _check(_lib.moe_balance_loss(
-        ctypes.byref(dims), _ptr(logits, "logits", torch.float32, (T, N)),
-        _ptr(topk_idx, "topk_idx", torch.int32, (T, k)),
-        _ptr(token_mask, "token_mask", torch.uint8, (T,), allow_none=True), float(alpha), float(z_coef),
-        _ptr(d_loss, "d_loss", torch.float32, None if d_loss is None or d_loss.dim() == 0 else (1,),
-             allow_none=True),
-        _ptr(counts, "counts", torch.int32, (N,)), _ptr(n_tokens, "n_tokens", torch.int32, (1,)),
-        _ptr(prob_mean, "prob_mean", torch.float32, (N,)), _ptr(loss, "loss", torch.float32, (3,)),
-        _ptr(d_logits, "d_logits", torch.float32, (T, N), allow_none=True),
-        _ptr(ws, "ws", torch.uint8), _nbytes(ws), _stream(stream)), "moe_balance_loss")
+        ctypes.byref(dims), _arg(logits, here, "logits", f32, (T, N)), _arg(topk_idx, here, "topk_idx", i32, (T, k)),
+        _opt(token_mask, here, "token_mask", torch.uint8, (T,)), alpha, z_coef,
+        _opt(d_loss, here, "d_loss", f32, () if d_loss is not None and d_loss.dim() == 0 else (1,)),
+        _arg(counts, here, "counts", i32, (N,)), _arg(n_tokens, here, "n_tokens", i32, (1,)),
+        _arg(prob_mean, here, "prob_mean", f32, (N,)), _arg(loss, here, "loss", f32, (3,)),
+        _opt(d_logits, here, "d_logits", f32, (T, N)), wp, wn, _stream_on(stream, here)), "moe_balance_loss")
 
 
 def router_backward_workspace_bytes(dims: Dims) -> int:
@@ -541,17 +556,13 @@ def router_backward(dims: Dims, x, w_router, d_logits, d_x, d_w_router, d_logit_
     """Gradient of the linear router for a dense gradient of the logits; outputs (each may be
     None) are written, or added to with accumulate (after backward_into)."""
     T, d, N = dims.T, dims.d_model, dims.n_experts
-    _one_device("x w_router d_logits d_x d_w_router d_logit_bias ws", x, w_router, d_logits, d_x,
-                d_w_router, d_logit_bias, ws)
+    here, f32 = _device(), torch.float32
+    wp, wn = _workspace(ws, here)
     _check(_lib.moe_router_backward(
-        ctypes.byref(dims), _ptr(x, "x", torch.bfloat16, (T, d)),
-        _ptr(w_router, "w_router", torch.float32, (N, d)),
-        _ptr(d_logits, "d_logits", torch.float32, (T, N)),
-        _ptr(d_x, "d_x", torch.float32, (T, d), allow_none=True),
-        _ptr(d_w_router, "d_w_router", torch.float32, (N, d), allow_none=True),
-        _ptr(d_logit_bias, "d_logit_bias", torch.float32, (N,), allow_none=True),
-        1 if accumulate else 0, _ptr(ws, "ws", torch.uint8), _nbytes(ws), _stream(stream)),
-        "moe_router_backward")
+        ctypes.byref(dims), _arg(x, here, "x", torch.bfloat16, (T, d)), _arg(w_router, here, "w_router", f32, (N, d)),
+        _arg(d_logits, here, "d_logits", f32, (T, N)), _opt(d_x, here, "d_x", f32, (T, d)),
+        _opt(d_w_router, here, "d_w_router", f32, (N, d)), _opt(d_logit_bias, here, "d_logit_bias", f32, (N,)),
+        1 if accumulate else 0, wp, wn, _stream_on(stream, here)), "moe_router_backward")
 
 
 class _Plan:
@@ -564,12 +575,14 @@ class _Plan:
         devices = {t.device for r in refs for t in r if t is not None}
         if len(devices) > 1:
             raise ValueError(f"the tensors are on several devices: {sorted(map(str, devices))}")
-        self.device = next(iter(devices), None)
+        device = next(iter(devices), None)
+        self.index = None if device is None else device.index
 
-    def check_device(self) -> None:
-        if self.device is not None and self.device.index != torch.cuda.current_device():
-            raise ValueError(f"the tensors are on {self.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
+    def check(self, kind, here: int, maker: str) -> None:
+        if self.array._type_ is not kind:
+            raise ValueError(f"this call takes a plan of {maker}()")
+        if self.index is not None and self.index != here:
+            raise ValueError(f"the plan's tensors are on cuda:{self.index}, the current device is cuda:{here}")
 
 
 def grad_plan(grads) -> _Plan:
@@ -592,13 +605,12 @@ def new_grad_norm_workspace(device=None) -> torch.Tensor:
 def grad_norm(plan: _Plan, max_norm: float, norm, scale, ws, stream=None) -> None:
     """norm [1]: the global norm of the plan's gradients; scale [1]: min(1, max_norm / (norm +
     1e-6)), or NaN (adamw_step then leaves the step out) where the norm is not finite."""
-    plan.check_device()
-    _one_device("norm scale ws", norm, scale, ws)
-    if plan.array._type_ is not GradTensor:
-        raise ValueError("grad_norm takes a plan of grad_plan()")
-    _check(_lib.moe_grad_norm(plan.array, plan.n, float(max_norm), _ptr(norm, "norm", torch.float32, (1,)),
-                              _ptr(scale, "scale", torch.float32, (1,)), _ptr(ws, "ws", torch.uint8),
-                              _nbytes(ws), _stream(stream)), "moe_grad_norm")
+    here = _device()
+    plan.check(GradTensor, here, "grad_plan")
+    wp, wn = _workspace(ws, here)
+    _check(_lib.moe_grad_norm(plan.array, plan.n, max_norm, _arg(norm, here, "norm", torch.float32, (1,)),
+                              _arg(scale, here, "scale", torch.float32, (1,)), wp, wn, _stream_on(stream, here)),
+           "moe_grad_norm")
 
 
 def new_adamw_state(param: torch.Tensor, bits: int = 32) -> dict:
@@ -656,14 +668,11 @@ def adamw_step(plan: _Plan, step, *, lr=1e-3, betas=(0.9, 0.999), eps: float = 1
     """One AdamW step over the plan's tensors. step: the number of this step, from 1, or an int32
     tensor [1] read when the kernel runs; lr: a number or an fp32 tensor [1] read likewise;
     grad_scale: fp32 tensor [1] (from grad_norm) or None."""
-    plan.check_device()
-    if plan.array._type_ is not AdamWTensor:
-        raise ValueError("adamw_step takes a plan of adamw_plan()")
+    here, f32 = _device(), torch.float32
+    plan.check(AdamWTensor, here, "adamw_plan")
     step_t = step if isinstance(step, torch.Tensor) else None
     lr_t = lr if isinstance(lr, torch.Tensor) else None
-    _one_device("step lr grad_scale", step_t, lr_t, grad_scale)
     cfg = AdamWConfig(0.0 if lr_t is not None else lr, betas[0], betas[1], eps, 1 if step_t is not None else step,
-                      seed & 0xFFFFFFFF, _ptr(step_t, "step", torch.int32, (1,), allow_none=True),
-                      _ptr(lr_t, "lr", torch.float32, (1,), allow_none=True),
-                      _ptr(grad_scale, "grad_scale", torch.float32, (1,), allow_none=True))
-    _check(_lib.moe_adamw_step(plan.array, plan.n, ctypes.byref(cfg), _stream(stream)), "moe_adamw_step")
+                      seed & 0xFFFFFFFF, _opt(step_t, here, "step", torch.int32, (1,)), _opt(lr_t, here, "lr", f32, (1,)),
+                      _opt(grad_scale, here, "grad_scale", f32, (1,)))
+    _check(_lib.moe_adamw_step(plan.array, plan.n, ctypes.byref(cfg), _stream_on(stream, here)), "moe_adamw_step")

@@ -222,3 +222,21 @@ def test_binding_refuses_before_any_call():
         moe.new_adamw_state(z(4), bits=4)
     s = moe.new_adamw_state(z(3, 43), bits=8)
     assert s["m"].dtype == torch.float8_e4m3fn and s["m_scale"].shape == (2,) and s["v"].numel() == 129
+
+
+def test_binding_names_the_argument_at_fault(monkeypatch):
+    """The calls' own checks on the host: what is wrong is named before the library is entered."""
+    monkeypatch.setattr(moe, "_device", lambda: 0)
+    d = _dims()
+    z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt)
+    args = [z(16, 8), z(16, 2, dt=torch.int32), None, z(8, dt=torch.int32), z(1, dt=torch.int32), z(8), z(3), None]
+    with pytest.raises(ValueError, match="ws must be a CUDA tensor"):
+        moe.balance_loss(d, *args, z(10, dt=torch.uint8))
+    with pytest.raises(ValueError, match="ws is required"):
+        moe.balance_loss(d, *args, None)
+    with pytest.raises(ValueError, match="ws must be"):
+        moe.router_backward(d, z(16, 128, dt=torch.bfloat16), z(8, 128), z(16, 8), None, None, None, z(10))
+    for call in (lambda: moe._arg(z(4), 0, "a", torch.float32, (4,)), lambda: moe._arg(z(4), -1, "a", torch.int32, (4,)),
+                 lambda: moe._arg(None, 0, "a", torch.float32, (4,)), lambda: moe._arg(z(4, 4).t(), -1, "a", torch.float32, (4, 4))):
+        with pytest.raises(ValueError, match="^a "):
+            call()
