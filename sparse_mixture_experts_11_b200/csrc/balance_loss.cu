@@ -29,6 +29,9 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBalThreads = 512;
 constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalPerSm = 1;
+// A lane with fewer values of a token than this takes two tokens at a time (T = 16384, device time in
+// us: N = 100 13.9, one at a time 16.5; N = 256, eight values a lane, 18.7 and 17.5).
+constexpr int kWide = 8;
 constexpr int kMaxN = 256;
 // Up to here every CTA counts all tokens' pairs itself (two rounds of its threads); past it they are
 // counted in chunks by a first launch. Device time of both, us: T = 1000, N = 64, k = 4 6.4 and
@@ -65,6 +68,8 @@ int balance_ctas(int64_t T, int N, int most) {
   const int per_cta = kBalWarps * (32 / token_shape(N).g);
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((T + per_cta - 1) / per_cta, most)));
 }
+// ints of a row of partial counts: N counts and the tokens, rounded up to four
+__host__ __device__ constexpr int count_ints(int N) { return (N + 4) / 4 * 4; }
 // floats of a CTA's row: N probabilities rounded up to four, then sum of lse^2 and padding
 __host__ __device__ constexpr int row_floats(int N) { return (N + 3) / 4 * 4 + 4; }
 
@@ -109,7 +114,8 @@ __global__ void __launch_bounds__(kBalThreads) balance_count_kernel(
   const int64_t t0 = blockIdx.x * chunk;
   count_pairs(topk_idx, mask, t0, min(static_cast<int64_t>(T), t0 + chunk), N, k, s_cnt);
   __syncthreads();
-  for (int e = threadIdx.x; e <= N; e += kBalThreads) rows[blockIdx.x * (N + 1) + e] = s_cnt[e];
+  for (int e = threadIdx.x; e < count_ints(N); e += kBalThreads)
+    rows[blockIdx.x * count_ints(N) + e] = e <= N ? s_cnt[e] : 0;
 }
 
 struct BalanceParams {
@@ -134,7 +140,8 @@ template <int G, int C, int VEC>
 __global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(const BalanceParams a) {
   constexpr int V = C * VEC;          // values a lane holds of a token
   constexpr int kGroups = 32 / G;     // tokens a warp takes at once
-  __shared__ int s_cnt[kMaxN + 1];
+  constexpr int U = V >= kWide ? 1 : 2;  // and rounds of them whose work overlaps
+  __shared__ int s_cnt[kMaxN + 4];
   __shared__ float s_acc[kBalWarps][G * V];
   __shared__ float s_z[kBalWarps];
   __shared__ float4 s_red[kBalThreads];
@@ -165,19 +172,31 @@ __global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(co
       }
     }
   };
-  float next[V];
-  load(t, next);  // under way while the counts are formed
+  // U tokens at a time: one's shuffles and exponentials fill the other's waits
+  float next[U][V];  // under way while the counts are formed
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(t + u * stride, next[u]);
   __syncthreads();
   if (a.n_count_rows == 0) {
     count_pairs(a.topk_idx, a.mask, 0, a.T, N, a.k, s_cnt);
   } else {
-    // threads of a column take every (kBalThreads / columns)-th row
-    const int cols = N + 1, groups = max(1, kBalThreads / cols);
-    for (int i = threadIdx.x; i < cols * groups; i += kBalThreads) {
-      int sum = 0;
+    // four columns a thread, and every (kBalThreads / quads)-th row
+    const int quads = count_ints(N) / 4, groups = kBalThreads / quads;
+    const int q = threadIdx.x % quads, g = threadIdx.x / quads;
+    if (g < groups) {
+      int4 sum = make_int4(0, 0, 0, 0);
 #pragma unroll 8
-      for (int r = i / cols; r < a.n_count_rows; r += groups) sum += __ldcg(a.count_rows + r * cols + i % cols);
-      if (sum != 0) atomicAdd(&s_cnt[i % cols], sum);
+      for (int r = g; r < a.n_count_rows; r += groups) {
+        const int4 v = __ldcg(reinterpret_cast<const int4*>(a.count_rows) + r * quads + q);
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+      }
+      const int c[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c[i] != 0) atomicAdd(&s_cnt[q * 4 + i], c[i]);
     }
   }
   __syncthreads();
@@ -198,51 +217,67 @@ __global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(co
     acc[j] = 0.f;
   }
   float z_acc = 0.f;
-  for (; t - lane / G < a.T; t += stride) {
-    float v[V];
-    float m = -INFINITY;
+  for (; t - lane / G < a.T; t += U * stride) {
+    float v[U][V], m[U], base[U], sum[U], inner[U];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      v[j] = next[j];
-      m = fmaxf(m, v[j]);
-    }
-    load(t + stride, next);
+    for (int u = 0; u < U; ++u) {
+      m[u] = -INFINITY;
 #pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    const float base = m == -INFINITY ? 0.f : m;  // a row of -inf only (or one that is not counted)
-    float sum = 0.f, inner = 0.f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      v[j] = expf(v[j] - base);
-      sum += v[j];
-      inner += v[j] * f[j];
+      for (int j = 0; j < V; ++j) {
+        v[u][j] = next[u][j];
+        m[u] = fmaxf(m[u], v[u][j]);
+      }
+      load(t + (U + u) * stride, next[u]);
     }
 #pragma unroll
     for (int o = G / 2; o > 0; o >>= 1) {
-      sum += __shfl_xor_sync(kFull, sum, o);
-      inner += __shfl_xor_sync(kFull, inner, o);
+#pragma unroll
+      for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(kFull, m[u], o));
     }
-    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-    const float lse = sum > 0.f ? base + logf(sum) : 0.f;
-    inner *= inv;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      v[j] *= inv;
-      acc[j] += v[j];
+    for (int u = 0; u < U; ++u) {
+      base[u] = m[u] == -INFINITY ? 0.f : m[u];  // a row of -inf only (or one that is not counted)
+      sum[u] = inner[u] = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        v[u][j] = expf(v[u][j] - base[u]);
+        sum[u] += v[u][j];
+        inner[u] += v[u][j] * f[j];
+      }
     }
-    if (gl == 0) z_acc += lse * lse;
-    if (a.d_logits != nullptr && t < a.T) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] *= c_bal * (f[j] - inner) + c_z * lse;
+    for (int o = G / 2; o > 0; o >>= 1) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int e = (c * G + gl) * VEC;
-        if (e < N) {
-          if (VEC == 4)
-            *reinterpret_cast<float4*>(a.d_logits + t * N + e) =
-                make_float4(v[c * VEC], v[c * VEC + VEC / 4], v[c * VEC + VEC / 2], v[c * VEC + VEC * 3 / 4]);
-          else
-            a.d_logits[t * N + e] = v[c];
+      for (int u = 0; u < U; ++u) {
+        sum[u] += __shfl_xor_sync(kFull, sum[u], o);
+        inner[u] += __shfl_xor_sync(kFull, inner[u], o);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float inv = sum[u] > 0.f ? 1.0f / sum[u] : 0.f;
+      const float lse = sum[u] > 0.f ? base[u] + logf(sum[u]) : 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        v[u][j] *= inv;
+        acc[j] += v[u][j];
+      }
+      if (gl == 0) z_acc += lse * lse;
+      const int64_t tok = t + u * stride;
+      if (a.d_logits != nullptr && tok < a.T) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[u][j] *= c_bal * (f[j] - inner[u] * inv) + c_z * lse;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const int e = (c * G + gl) * VEC;
+          if (e < N) {
+            if (VEC == 4)
+              *reinterpret_cast<float4*>(a.d_logits + tok * N + e) =
+                  make_float4(v[u][c * VEC], v[u][c * VEC + VEC / 4], v[u][c * VEC + VEC / 2],
+                              v[u][c * VEC + VEC * 3 / 4]);
+            else
+              a.d_logits[tok * N + e] = v[u][c];
+          }
         }
       }
     }
@@ -350,8 +385,8 @@ __global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(co
 
 size_t balance_scratch_bytes(int64_t T, int N) {
   if (T == 0) return 0;
-  const size_t rows = static_cast<size_t>(count_plan(T).rows) * (N + 1) * sizeof(int32_t);
-  return (rows + 15) / 16 * 16 +
+  const size_t rows = static_cast<size_t>(count_plan(T).rows) * count_ints(N) * sizeof(int32_t);
+  return rows +
          static_cast<size_t>(balance_ctas(T, N, kBalanceMaxCtas)) * row_floats(N) *
              sizeof(float);
 }
@@ -376,7 +411,7 @@ cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
   p.count_rows = static_cast<const int32_t*>(a.scratch);
   p.n_count_rows = cp.rows;
   p.part = reinterpret_cast<float*>(static_cast<char*>(a.scratch) +
-                                    (static_cast<size_t>(cp.rows) * (a.N + 1) * 4 + 15) / 16 * 16);
+                                    static_cast<size_t>(cp.rows) * count_ints(a.N) * 4);
   p.counter = a.counter;
   p.T = a.T;
   p.N = a.N;
