@@ -236,7 +236,22 @@ __device__ __forceinline__ float2 mul2_rn(float2 a, float b) {
 __device__ __forceinline__ float2 add2_rn(float2 a, float2 b) {
   return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
 }
+// The largest of three; NaN where one is (fmaxf would drop it, and a block's scale hide it).
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Two bf16, each rounded up in magnitude with the probability of the part that is cut off: the 16
+// random bits (rbits' low half for x, high for y) are added to the bits and the sum is cut, except
+// that a NaN stays one.
+__device__ __forceinline__ uint32_t bf16x2_by_chance(float2 a, uint32_t rbits) {
+  uint32_t d;
+  asm("cvt.rs.bf16x2.f32 %0, %1, %2, %3;" : "=r"(d) : "f"(a.y), "f"(a.x), "r"(rbits));
+  return d;
+}
 
 // E4M3 rounding, up with the probability of the part that is cut off. z = x 2^-120 for |x| <= 448:
 // x = 2^-6, E4M3's smallest normal, becomes 2^-126, fp32's, and the subnormals of the two formats
@@ -407,16 +422,15 @@ __device__ __forceinline__ void adam_block(const AdamEntry& t, const StepScalars
     store4<FULL>(static_cast<uint16_t*>(t.param) + i, rem, pack_bf16x2(p[0].x, p[0].y),
                  pack_bf16x2(p[1].x, p[1].y));
   } else {
-    const float pv[4] = {p[0].x, p[0].y, p[1].x, p[1].y};
-    uint32_t up[4];
+    uint32_t u[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) up[q] = __float_as_uint(pv[q]) + ((h[q] * 0xD1B54A35u + key) >> 16);
-    store4<FULL>(static_cast<uint16_t*>(t.param) + i, rem, __byte_perm(up[0], up[1], 0x7632),
-                 __byte_perm(up[2], up[3], 0x7632));
+    for (int q = 0; q < 4; ++q) u[q] = h[q] * 0xD1B54A35u + key;
+    store4<FULL>(static_cast<uint16_t*>(t.param) + i, rem, bf16x2_by_chance(p[0], __byte_perm(u[0], u[1], 0x7632)),
+                 bf16x2_by_chance(p[1], __byte_perm(u[2], u[3], 0x7632)));
   }
   if (BITS8) {
-    const float ma4 = fmaxf(fmaxf(fabsf(m[0].x), fabsf(m[0].y)), fmaxf(fabsf(m[1].x), fabsf(m[1].y)));
-    const float ra4 = fmaxf(fmaxf(r[0].x, r[0].y), fmaxf(r[1].x, r[1].y));
+    const float m1 = fabsf(m[1].y), ma4 = max3_nan(fabsf(m[0].x), fabsf(m[0].y), max3_nan(fabsf(m[1].x), m1, m1));
+    const float ra4 = max3_nan(r[0].x, r[0].y, max3_nan(r[1].x, r[1].y, r[1].y));
     const float ma = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(ma4)));
     const float ra = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(ra4)));
     // a block below 2^-96 (its reciprocal could overflow) is kept as zeros: codes and scale

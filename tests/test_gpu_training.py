@@ -472,6 +472,29 @@ def test_adamw_leaves_the_step_out(kind):
         assert before[k] is None or np.array_equal(before[k], after[k]), k
 
 
+@pytest.mark.parametrize("kind", KINDS, ids=lambda k: f"{k[0]}-{str(k[1])[6:]}-{k[2]}")
+def test_adamw_keeps_a_nan(kind):
+    """Without grad_scale a NaN gradient is not left out: its element's parameter becomes NaN (and
+    stays it), no other parameter does, and a block's 8-bit moments become NaN by their scale."""
+    n, at = 1000, [0, 129, 131, 701, 999]
+    t = make_tensor(n, kind, seed=1)
+    t["grad"][at] = float("nan")
+    plan = moe.adamw_plan([descriptor(t)])
+    moe.adamw_step(plan, 1, seed=5)
+    for name in ("param", "master"):
+        if t[name] is not None:
+            assert torch.isnan(t[name]).nonzero().flatten().tolist() == at
+    if kind[2] == 8:
+        for name in ("m_scale", "v_scale"):
+            assert torch.isnan(t[name]).nonzero().flatten().tolist() == sorted({i // 128 for i in at})
+    else:
+        for name in ("m", "v"):
+            assert torch.isnan(t[name]).nonzero().flatten().tolist() == at
+    t["grad"].zero_()
+    moe.adamw_step(plan, 2, seed=5)
+    assert bool(torch.isnan(t["param"][at]).all())
+
+
 def test_adamw_step_and_rate_on_the_device_replayed():
     """A captured step with the step number, rate and scale on the device, replayed, equals steps
     called one by one with numbers."""
