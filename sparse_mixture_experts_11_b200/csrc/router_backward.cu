@@ -711,8 +711,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // tile's epilogue runs beside the next one's MMAs. A lane holds a token, so scaling back is one
 // factor a lane; 32 x 32 blocks go through shared memory to TMA stores. Accumulating is the same
 // store as a reduction: the L2 adds (one addition an element, so the order is fixed) and no SM
-// waits for the old values. (Lanes along c, and 128-byte reductions from registers: 299 us at
-// T = 16384, N = 256, d = 7168, bound by the issue of the reductions.)
+// waits for the old values, which are called to the L2 a tile ahead (T = 16384, dL's and W_r's
+// terms included: N = 32, d = 2880 86 us, 102 without; N = 256, d = 7168 221 and 235). (Lanes along
+// c, and 128-byte reductions from registers: 299 us for the latter, bound by their issue.)
 constexpr int kXStages = 3;
 constexpr int kXStageBytes = 2 * kXTileT * kKb * 2 + 2 * (kXTileC / 64) * kBox;
 constexpr int kXStaging = 32 * 32 * 4;  // one block; two for each epilogue warp
@@ -726,11 +727,15 @@ __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, uint32
                : "memory");
 }
 
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 __global__ void __launch_bounds__(kTcThreads, 1)
     router_dgrad_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_dl,
-                        const __grid_constant__ CUtensorMap tm_out, const int32_t* __restrict__ row_exp, int64_t T,
-                        int N, int d, int c_tiles, int64_t tiles, int accumulate, int* status,
-                        uint64_t timeout_ns) {
+                        const __grid_constant__ CUtensorMap tm_out, const float* out,
+                        const int32_t* __restrict__ row_exp, int64_t T, int N, int d, int c_tiles, int64_t tiles,
+                        int accumulate, int* status, uint64_t timeout_ns) {
   extern __shared__ __align__(1024) uint8_t dyn_smem[];
   __shared__ TcShared sh;
   pdl_trigger();
@@ -822,12 +827,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int q = warp & 3;            // TMEM lane quadrant: tokens q * 32 .. of the tile
     const int half = (warp - 2) >> 2;  // columns [half * 128, half * 128 + 128) of the tile
     const uint32_t stage0 = base + kXStages * kXStageBytes + (warp - 2) * 2 * kXStaging;
+    // old values of this warp's part of a tile, one row a lane, to the L2
+    auto ahead = [&](int64_t t) {
+      if (!accumulate || t >= tiles) return;
+      const int64_t r0 = t / c_tiles * kXTileT + q * 32;
+      const int c0 = static_cast<int>(t % c_tiles) * kXTileC + half * 128;
+      if (c0 < d && r0 + lane < T) l2_prefetch(out + (r0 + lane) * d + c0, min(128, d - c0) * 4);
+    };
+    ahead(blockIdx.x);
     int uc = 0, n = 0;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++uc) {
       const int buf = uc & 1;
       const int64_t r0 = t / c_tiles * kXTileT + q * 32;
       const int c0 = static_cast<int>(t % c_tiles) * kXTileC + half * 128;
       const int e = r0 + lane < T ? row_exp[r0 + lane] : 0;
+      ahead(t + gridDim.x);
       // 2^(a_t - 28) in two factors, the second 1 but for tokens below 2^-98
       const float f = scalbnf(1.0f, min(127, max(-126, e - 28)));
       const float f2 = scalbnf(1.0f, max(-149, min(0, e - 28 + 126)));
@@ -971,8 +985,8 @@ cudaError_t launch_tc(const RouterBackwardArgs& a, cudaStream_t s) {
     const int64_t tiles = c_tiles * ((static_cast<int64_t>(a.T) + kXTileT - 1) / kXTileT);
     const int grid = static_cast<int>(std::min<int64_t>(tiles, di.sm_count));
     e = launch_pdl(router_dgrad_kernel, dim3(grid), dim3(kTcThreads), kXSmem, s, mw, mdl, mo,
-                   static_cast<const int32_t*>(row_exp), static_cast<int64_t>(a.T), a.N, a.d, c_tiles, tiles,
-                   a.accumulate, a.status, a.timeout_ns);
+                   static_cast<const float*>(a.d_x), static_cast<const int32_t*>(row_exp),
+                   static_cast<int64_t>(a.T), a.N, a.d, c_tiles, tiles, a.accumulate, a.status, a.timeout_ns);
     if (e != cudaSuccess) return e;
   }
   if (!want_w && !want_b) return cudaSuccess;
