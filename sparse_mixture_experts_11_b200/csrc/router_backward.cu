@@ -199,14 +199,18 @@ __global__ void __launch_bounds__(kThreads) router_backward_kernel(const Params 
   else x_tile(a, s_dl);
 }
 
-// The token ranges' partial sums. CTAs [0, w_ctas): 64 float4s of dW_r each, four threads a float4
-// over a quarter of the ranges, whose sums are added in order; the bias gradient's by a warp an
-// expert, 32 strided sums and their tree.
-constexpr int kSumItems = 64;
+// The token ranges' partial sums. CTAs [0, w_ctas): 256 / SPLIT float4s of dW_r each, SPLIT threads a
+// float4 over a part of the ranges each, whose sums are added in order; the bias gradient's by a
+// warp an expert, 32 strided sums and their tree.
+// Up to here a float4 takes one thread. Device time of dW, one thread and four, us: 5 ranges of 256 x 7168
+// 142.6, 145.0; 8 of 64 x 1024 8.8, 9.2; 24 of 64 x 2048 33.6, 32.1; 36 of 32 x 2880 47, 36.
+constexpr int kSumAlone = 8;
+template <int SPLIT>
 __global__ void __launch_bounds__(256) router_backward_sum_kernel(
     const float* __restrict__ part_w, const float* __restrict__ part_b, float* __restrict__ d_w,
     float* __restrict__ d_b, int chunks, int b_parts, int N, int d, int accumulate, int w_ctas) {
-  __shared__ float4 s_part[4][kSumItems];
+  constexpr int kItems = 256 / SPLIT;
+  __shared__ float4 s_part[SPLIT][kItems];
   pdl_trigger();
   pdl_wait();
   if (static_cast<int>(blockIdx.x) >= w_ctas) {
@@ -221,13 +225,15 @@ __global__ void __launch_bounds__(256) router_backward_sum_kernel(
     return;
   }
   const int64_t items = static_cast<int64_t>(N) * d / 4;
-  const int quarter = threadIdx.x / kSumItems, j = threadIdx.x % kSumItems;
-  const int64_t i = blockIdx.x * static_cast<int64_t>(kSumItems) + j;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int part = threadIdx.x / kItems, j = threadIdx.x % kItems;
+  const int64_t i = blockIdx.x * static_cast<int64_t>(kItems) + j;
+  float4* out = reinterpret_cast<float4*>(d_w) + i;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f), old = s;
   if (i < items) {
-    const int c1 = chunks * (quarter + 1) / 4;
+    if (accumulate && part == 0) old = __ldcs(out);
+    const int c1 = chunks * (part + 1) / SPLIT;
 #pragma unroll 8
-    for (int c = chunks * quarter / 4; c < c1; ++c) {
+    for (int c = chunks * part / SPLIT; c < c1; ++c) {
       const float4 v = __ldcs(reinterpret_cast<const float4*>(part_w) + c * items + i);
       s.x += v.x;
       s.y += v.y;
@@ -235,35 +241,39 @@ __global__ void __launch_bounds__(256) router_backward_sum_kernel(
       s.w += v.w;
     }
   }
-  s_part[quarter][j] = s;
-  __syncthreads();
-  if (quarter != 0 || i >= items) return;
+  if (SPLIT > 1) {
+    s_part[part][j] = s;
+    __syncthreads();
+    if (part != 0) return;
 #pragma unroll
-  for (int q = 1; q < 4; ++q) {
-    const float4 v = s_part[q][j];
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
+    for (int q = 1; q < SPLIT; ++q) {
+      const float4 v = s_part[q][j];
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
   }
-  float4* out = reinterpret_cast<float4*>(d_w) + i;
-  if (accumulate) {
-    const float4 old = *out;
-    s.x += old.x;
-    s.y += old.y;
-    s.z += old.z;
-    s.w += old.w;
-  }
+  if (i >= items) return;
+  if (accumulate) s = make_float4(s.x + old.x, s.y + old.y, s.z + old.z, s.w + old.w);
   *out = s;
+}
+
+template <int SPLIT>
+cudaError_t launch_sum_split(const float* part_w, const float* part_b, const RouterBackwardArgs& a, int chunks,
+                             int b_parts, cudaStream_t s) {
+  constexpr int kItems = 256 / SPLIT;
+  const int64_t items = static_cast<int64_t>(a.N) * a.d / 4;
+  const int w_ctas = a.d_w_router != nullptr ? static_cast<int>((items + kItems - 1) / kItems) : 0;
+  const int b_ctas = a.d_logit_bias != nullptr ? (a.N + 7) / 8 : 0;
+  return launch_pdl(router_backward_sum_kernel<SPLIT>, dim3(w_ctas + b_ctas), dim3(256), 0, s, part_w, part_b,
+                    a.d_w_router, a.d_logit_bias, chunks, b_parts, a.N, a.d, a.accumulate, w_ctas);
 }
 
 cudaError_t launch_sum(const float* part_w, const float* part_b, const RouterBackwardArgs& a, int chunks,
                        int b_parts, cudaStream_t s) {
-  const int64_t items = static_cast<int64_t>(a.N) * a.d / 4;
-  const int w_ctas = a.d_w_router != nullptr ? static_cast<int>((items + kSumItems - 1) / kSumItems) : 0;
-  const int b_ctas = a.d_logit_bias != nullptr ? (a.N + 7) / 8 : 0;
-  return launch_pdl(router_backward_sum_kernel, dim3(w_ctas + b_ctas), dim3(256), 0, s, part_w, part_b,
-                    a.d_w_router, a.d_logit_bias, chunks, b_parts, a.N, a.d, a.accumulate, w_ctas);
+  return chunks <= kSumAlone ? launch_sum_split<1>(part_w, part_b, a, chunks, b_parts, s)
+                             : launch_sum_split<4>(part_w, part_b, a, chunks, b_parts, s);
 }
 
 // ------------------------------------------------------------------ tensor-core path
