@@ -29,7 +29,7 @@
 // apart, and a block's next scale can hang on one code. So every fp32 operation is rounded by
 // itself, in the order of the formulas (no fused multiply-add; square root, quotient and
 // reciprocal to nearest): any fp32 implementation of these lines has the same results, bit by bit.
-// 537M elements with masters take 2365 us so, 2305 with approximate roots and quotients.
+// 537M elements with masters took 2365 us so and 2305 with approximate roots and quotients.
 #include <math.h>
 
 #include <algorithm>
@@ -45,7 +45,8 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kOptThreads = 256;
 constexpr int kOptWarps = kOptThreads / 32;
 // Mixed lists up to here (in tiles) take one launch for both kinds of moments. Device time of one
-// launch and of two, us: 384 tiles 5.1, 9.8; 1930 tiles 21.0, 25.1; 6146 tiles 51.9, 54.2; 24584 tiles 224.8, 223.2.
+// launch and of two, us: 384 tiles 5.1, 9.8; 1930 tiles 19.0, 22.8; 6146 tiles 50.3, 53.3; 36888 tiles
+// 308.9, 287.5 (24584 tiles with masters 208.0, 221.5).
 constexpr int64_t kBothTiles = 8192;
 constexpr int kTileBlocks = 2 * kOptWarps;  // a tile: two blocks for each warp of a CTA
 constexpr int64_t kMaxChunks = 1 << 30;  // of a launch: a kernel's chunk index plus its grid is an int
@@ -618,9 +619,9 @@ cudaError_t launch_adamw_kind(const moe_adamw_tensor* tensors, int n, int64_t to
                               cudaStream_t s) {
   // fp32 moments: a CTA a tile, in the tensor's order. What bounds the kernel is how well the
   // memory streams, and CTAs that start in order keep all SMs within a few pages of each other
-  // (537M elements with masters: 2377 us; persistent CTAs on chunks of 16 tiles, 2696 us).
+  // (537M elements with masters: 2348 us; persistent CTAs on chunks of 16 tiles, 2687 us).
   // 8 bits: as many CTAs as are resident, on chunks that grow with the total: here instructions
-  // bound, and a CTA's start is a part of a tile's (1770 us; a CTA a tile, 1911 us).
+  // bound, and a CTA's start is a part of a tile's (1775 us; a CTA a tile, 1877 us).
   const int64_t resident = static_cast<int64_t>(sms) * 4;
   int chunk_tiles = 1;
   while (KIND == kMoments8 && chunk_tiles < 32 && total / chunk_tiles > 8 * resident) chunk_tiles *= 2;
