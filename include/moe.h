@@ -52,6 +52,7 @@
  *       MOE_ERR_BOUNDS       a row index computed from device data fell outside its buffer
  *                            (the access is skipped)
  *     moe_read_device_error() reads and clears that word.
+ *   - A workspace serves one call at a time: calls that may overlap on the GPU take one each.
  *   - Inputs must be finite; results for NaN or Inf inputs are unspecified.
  */
 #ifndef MOE_H_
@@ -386,7 +387,8 @@ typedef struct {
 } moe_grad_tensor;
 
 /* Global norm of n gradients and the scale that clips it:
- *   norm  [1] fp32 (out)   sqrt(sum of the squares of all elements)
+ *   norm  [1] fp32 (out)   sqrt(sum of the squares of all elements; each square in fp32, so one
+ *                          below 2^-149 adds nothing)
  *   scale [1] fp32 (out)   min(1, max_norm / (norm + 1e-6)); NaN if norm is not finite (a NaN or
  *                          an infinity among the gradients, or squares past fp32's range), which
  *                          makes moe_adamw_step leave the step out. max_norm > 0, may be infinite
@@ -411,7 +413,8 @@ moe_status moe_grad_norm(const moe_grad_tensor* tensors, int32_t n, float max_no
  *                value is rounded up with the probability of what is cut off; a nonzero v keeps a
  *                nonzero code; a block whose largest magnitude is below 2^-96 becomes zeros. This
  *                step's update uses the moments before that rounding. All zeros to begin with
- *   m_scale, v_scale  [ceil(numel / MOE_ADAMW_BLOCK)] fp32 (4-byte aligned), state_bits 8 only */
+ *   m_scale, v_scale  [ceil(numel / MOE_ADAMW_BLOCK)] fp32 (4-byte aligned), state_bits 8 only
+ * A NaN in a gradient makes its parameter NaN and its moments, with 8 bits those of its block. */
 typedef struct {
   void* param;
   float* master;
@@ -441,10 +444,11 @@ typedef struct {
 /* One AdamW step (decoupled weight decay) over n tensors at once:
  *   g' = g grad_scale,  m' = beta1 m + (1 - beta1) g',  v' = beta2 v + (1 - beta2) g'^2,
  *   p' = p (1 - lr wd) - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
- * in fp32, each operation rounded by itself, in this order. The random bits of a rounding depend on seed, t, the tensor's place in the list and
- * the element, so equal calls give equal results. `tensors` and `config` are host memory, read
- * during the call; a graph that captures the call keeps the pointers that they held. A launch
- * takes up to 384 tensors, and large lists a launch for each kind of moments. No workspace. */
+ * in fp32, each operation rounded by itself, in this order. The random bits of a rounding depend
+ * on seed, t, the tensor's place in the list and the element, so equal calls give equal results.
+ * `tensors` and `config` are host memory, read during the call; a graph that captures the call
+ * keeps the pointers that they held. A launch takes up to 384 tensors, and large lists a launch
+ * for each kind of moments. No workspace. */
 moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n,
                           const moe_adamw_config* config, void* stream);
 
