@@ -340,6 +340,15 @@ __host__ __device__ constexpr int w_stages(int group) {
   return (kTcMaxSmem - 1024) / w_stage_bytes(group) < 8 ? (kTcMaxSmem - 1024) / w_stage_bytes(group) : 8;
 }
 
+// Lanes a token takes in split_dl_kernel and pairs of values a lane holds: 2 g p >= N.
+struct SplitShape {
+  int g, p;
+};
+SplitShape split_shape(int N) {
+  return N <= 8 ? SplitShape{4, 1} : N <= 16 ? SplitShape{8, 1} : N <= 32 ? SplitShape{16, 1}
+       : N <= 64 ? SplitShape{32, 1} : N <= 128 ? SplitShape{32, 2} : SplitShape{32, 4};
+}
+
 TcPlan make_tc_plan(int64_t T, int N, int d) {
   TcPlan p{};
   p.np = (N + 7) / 8 * 8;
@@ -360,7 +369,8 @@ TcPlan make_tc_plan(int64_t T, int N, int d) {
     }
   }
   p.chunks = static_cast<int>((T + p.chunk - 1) / p.chunk);
-  p.split_rows = static_cast<int>(std::max<int64_t>(8, (T + 591) / 592));
+  const int64_t round = kThreads / split_shape(N).g;  // tokens that a CTA splits at once
+  p.split_rows = static_cast<int>(((T + 591) / 592 + round - 1) / round * round);
   p.split_ctas = static_cast<int>((T + p.split_rows - 1) / p.split_rows);
   auto r256 = [](size_t v) { return (v + 255) / 256 * 256; };
   p.dl16_bytes = r256(static_cast<size_t>(2) * T * p.np * 2);
@@ -431,50 +441,56 @@ __global__ void __launch_bounds__(kThreads) split_w_kernel(const float* __restri
   }
 }
 
-// A warp a token: dL's row as two scaled fp16 terms [2][T][np] with a_t (for dx; w_exp null: left
-// out) and as three bf16 terms [3][T][np] (for dW; dl_terms null: left out); the CTA's sums over its
-// tokens for the bias.
+// G lanes a token, P pairs of values a lane (2 G P >= N): dL's row as two scaled fp16 terms [2][T][np]
+// with a_t (for dx; w_exp null: left out) and as three bf16 terms [3][T][np] (for dW; dl_terms null: left
+// out); the CTA's sums over its tokens for the bias. (A warp a token whatever N: the whole call 49 us and
+// not 43 at T = 16384, N = 8, d = 1024; 34 and not 28 at d = 512.)
+template <int G, int P>
 __global__ void __launch_bounds__(kThreads) split_dl_kernel(
     const float* __restrict__ dl, const int32_t* __restrict__ w_exp, uint16_t* __restrict__ dl16,
     int32_t* __restrict__ row_exp, uint16_t* __restrict__ dl_terms, float* __restrict__ bias_part, int64_t T,
     int N, int np, int rows) {
-  __shared__ float s_sum[kThreads / 32][256];
+  constexpr int kTokens = kThreads / G;  // of a round
+  __shared__ float s_sum[kThreads / 32][2 * G * P];
   pdl_trigger();
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane % G;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * rows, t1 = min(T, t0 + rows);
   const int64_t plane = T * np;
-  float acc[8];
-  int b[8];
+  float acc[2 * P];
+  int b[2 * P];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    // values 2 j, 2 j + 1 of this lane: experts j * 64 + lane * 2 and the next
-    const int n = j * 64 + lane * 2;
+  for (int j = 0; j < P; ++j) {
+    // values 2 j, 2 j + 1 of this lane: experts (j * G + gl) * 2 and the next
+    const int n = (j * G + gl) * 2;
     acc[2 * j] = acc[2 * j + 1] = 0.f;
     b[2 * j] = w_exp != nullptr && n < N ? w_exp[n] : 0;
     b[2 * j + 1] = w_exp != nullptr && n + 1 < N ? w_exp[n + 1] : 0;
   }
-  for (int64_t t = t0 + warp; t < t1; t += kThreads / 32) {
-    float v[8];
+  for (int64_t tb = t0; tb < t1; tb += kTokens) {
+    const int64_t t = tb + threadIdx.x / G;
+    const bool live = t < t1;
+    float v[2 * P];
     int top = -1000;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = j * 64 + lane * 2;
-      v[2 * j] = n < N ? dl[t * N + n] : 0.f;
-      v[2 * j + 1] = n + 1 < N ? dl[t * N + n + 1] : 0.f;
+    for (int j = 0; j < P; ++j) {
+      const int n = (j * G + gl) * 2;
+      v[2 * j] = live && n < N ? dl[t * N + n] : 0.f;
+      v[2 * j + 1] = live && n + 1 < N ? dl[t * N + n + 1] : 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 2 * P; ++j) {
       acc[j] += v[j];
       if (v[j] != 0.f) top = max(top, exponent_of(v[j]) + b[j]);
     }
     if (w_exp != nullptr) {
-      top = __reduce_max_sync(kFull, top);
-      if (lane == 0) row_exp[t] = top;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = j * 64 + lane * 2;
-        if (n >= np) break;
+      for (int o = G / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+      if (gl == 0 && live) row_exp[t] = top;
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        const int n = (j * G + gl) * 2;
+        if (n >= np || !live) break;
         float x = scale_by(v[2 * j], 14 + b[2 * j] - top), y = scale_by(v[2 * j + 1], 14 + b[2 * j + 1] - top);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -485,9 +501,9 @@ __global__ void __launch_bounds__(kThreads) split_dl_kernel(
     }
     if (dl_terms != nullptr) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = j * 64 + lane * 2;
-        if (n >= np) break;
+      for (int j = 0; j < P; ++j) {
+        const int n = (j * G + gl) * 2;
+        if (n >= np || !live) break;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
           const uint32_t lo = bf16_term(v[2 * j]), hi = bf16_term(v[2 * j + 1]);
@@ -498,7 +514,14 @@ __global__ void __launch_bounds__(kThreads) split_dl_kernel(
   }
   if (bias_part == nullptr) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s_sum[warp][j / 2 * 64 + lane * 2 + j % 2] = acc[j];
+  for (int o = G; o < 32; o <<= 1) {
+#pragma unroll
+    for (int j = 0; j < 2 * P; ++j) acc[j] += __shfl_xor_sync(kFull, acc[j], o);
+  }
+  if (lane < G) {
+#pragma unroll
+    for (int j = 0; j < 2 * P; ++j) s_sum[warp][(j / 2 * G + gl) * 2 + j % 2] = acc[j];
+  }
   __syncthreads();
   for (int n = threadIdx.x; n < N; n += kThreads) {
     float s = 0.f;
@@ -906,9 +929,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // Tensor cores where the products are worth the five launches, from T N d = 2^26 on. Device time
-// of the two paths, CUDA cores first, us, at (T, d, N): (256, 1024, 64) 12.1, 18.4; (512, 2880, 32) 15.2,
-// 18.8; (1024, 1024, 64) 18.1, 20.5; (64, 4096, 256) 26.4, 24.0; (4096, 512, 64) 30.4, 22.2;
-// (4096, 2880, 32) 70, 30; (1024, 4096, 128) 83, 26. Below 64 tokens a row block of the MMA is half empty.
+// of the two paths, CUDA cores first, us, at (T, d, N): (256, 1024, 64) 11.3, 18.3; (512, 2880, 32) 15.9,
+// 19.5; (1024, 1024, 64) 18.1, 20.1; (16384, 512, 8) 27.6, 27.9; (64, 4096, 256) 26.5, 22.6; (4096, 512, 64)
+// 30.2, 22.8; (4096, 2880, 32) 69, 32; (1024, 4096, 128) 83, 24. Below 64 tokens a row block of the MMA
+// is half empty.
 bool use_tensor_cores(int64_t T, int N, int d) { return T >= 64 && static_cast<double>(T) * N * d >= 67108864.0; }
 
 template <int GROUP>
@@ -949,7 +973,11 @@ cudaError_t launch_tc(const RouterBackwardArgs& a, cudaStream_t s) {
     e = launch_pdl(split_w_kernel, dim3(a.N), dim3(kThreads), 0, s, a.w_router, w_terms, w_exp, a.N, a.d);
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(split_dl_kernel, dim3(p.split_ctas), dim3(kThreads), 0, s, a.d_logits,
+  const SplitShape ss = split_shape(a.N);
+  auto* split = ss.g == 4 ? split_dl_kernel<4, 1> : ss.g == 8 ? split_dl_kernel<8, 1>
+              : ss.g == 16 ? split_dl_kernel<16, 1> : ss.p == 1 ? split_dl_kernel<32, 1>
+              : ss.p == 2 ? split_dl_kernel<32, 2> : split_dl_kernel<32, 4>;
+  e = launch_pdl(split, dim3(p.split_ctas), dim3(kThreads), 0, s, a.d_logits,
                  want_x ? static_cast<const int32_t*>(w_exp) : nullptr, dl16, row_exp, want_w ? dl_terms : nullptr,
                  want_b ? bias_part : nullptr, static_cast<int64_t>(a.T), a.N, p.np, p.split_rows);
   if (e != cudaSuccess) return e;

@@ -220,7 +220,7 @@ ROUTER_CASES = [(1, 64, 1), (1, 128, 256), (3, 64, 5), (64, 128, 8), (65, 192, 7
                 (257, 1024, 64), (512, 448, 130), (1000, 320, 33), (700, 7168, 17), (4096, 1024, 64),
                 (2049, 640, 256), (5000, 256, 100), (16384, 512, 31), (8192, 4096, 8),
                 (2001, 2880, 7), (1537, 448, 130), (300, 576, 200), (16384, 64, 256), (260, 4096, 40),
-                (64, 4096, 256), (101, 5760, 130), (3000, 2880, 9)]
+                (64, 4096, 256), (101, 5760, 130), (3000, 2880, 9), (5003, 4096, 5), (2999, 1024, 37)]
 
 
 @pytest.mark.parametrize("T,d,N", ROUTER_CASES)
