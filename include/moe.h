@@ -348,7 +348,8 @@ moe_status moe_backward(const moe_dims* dims, const uint16_t* x, const float* w_
  *   counts      [N] int32 (out)          c_e
  *   n_tokens    [1] int32 (out)          n. With n = 0 every other output is zero
  *   prob_mean   [N] fp32 (out)           P_e
- *   loss        [3] fp32 (out)           balance + z, balance, z
+ *   loss        [3] fp32 (out)           balance + z, balance, z (infinite only where z itself is
+ *                                        past fp32's range; 0 with z_coef = 0, whatever lse is)
  *   d_logits    [T, N] fp32 (out) or NULL; must not overlap logits
  * Deterministic. Uses the per-stage workspace (moe_workspace_bytes). T == 0 launches nothing and
  * writes nothing, as everywhere. */

@@ -38,6 +38,11 @@ constexpr int kMaxN = 256;
 // 7.7; T = 2048, k = 4 8.0 and 8.6; T = 4096, k = 1 11.0 and 9.9; k = 4 11.5 and 10.3.
 constexpr int64_t kInlineTokens = 2048;
 constexpr int kCountRows = 64;  // rows of partial counts, at most
+// lse^2 passes fp32's range where |lse| does 1.8e19 (a counted row of the type's lowest value), and the
+// loss divides the sum by n and may multiply it by 0. So there are two sums: the squares below 2^96, and
+// those of the larger |lse| times 2^-80. Neither overflows for any number of tokens (2^31 of at most
+// 2^96), and what the first has under 2^96 the second has as normal numbers.
+constexpr float kFarLse = 0x1p48f, kFarScale = 0x1p-80f;
 
 struct CountPlan {
   int64_t chunk;  // tokens a row
@@ -70,7 +75,7 @@ int balance_ctas(int64_t T, int N, int most) {
 }
 // ints of a row of partial counts: N counts and the tokens, rounded up to four
 __host__ __device__ constexpr int count_ints(int N) { return (N + 4) / 4 * 4; }
-// floats of a CTA's row: N probabilities rounded up to four, then sum of lse^2 and padding
+// floats of a CTA's row: N probabilities rounded up to four, then the two sums of lse^2 and padding
 __host__ __device__ constexpr int row_floats(int N) { return (N + 3) / 4 * 4 + 4; }
 
 // Counts of tokens [t0, t1): pairs of counted tokens that chose expert e into s_cnt[e], counted
@@ -143,7 +148,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(co
   constexpr int U = V >= kWide ? 1 : 2;  // and rounds of them whose work overlaps
   __shared__ int s_cnt[kMaxN + 4];
   __shared__ float s_acc[kBalWarps][G * V];
-  __shared__ float s_z[kBalWarps];
+  __shared__ float s_z[2][kBalWarps];  // the two sums of lse^2
   __shared__ float4 s_red[kBalThreads];
   __shared__ int s_last;
   const int N = a.N;
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(co
     f[j] = e < N ? static_cast<float>(s_cnt[e]) * inv_n : 0.f;
     acc[j] = 0.f;
   }
-  float z_acc = 0.f;
+  float z_near = 0.f, z_far = 0.f;
   for (; t - lane / G < a.T; t += U * stride) {
     float v[U][V], m[U], base[U], sum[U], inner[U];
 #pragma unroll
@@ -262,7 +267,12 @@ __global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(co
         v[u][j] *= inv;
         acc[j] += v[u][j];
       }
-      if (gl == 0) z_acc += lse * lse;
+      if (gl == 0) {
+        const bool far = fabsf(lse) >= kFarLse;
+        const float x = far ? lse * kFarScale : lse;
+        if (far) z_far += x * x;
+        else z_near += x * x;
+      }
       const int64_t tok = t + u * stride;
       if (a.d_logits != nullptr && tok < a.T) {
 #pragma unroll
@@ -289,12 +299,18 @@ __global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(co
     for (int j = 0; j < V; ++j) acc[j] += __shfl_xor_sync(kFull, acc[j], o);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) z_acc += __shfl_xor_sync(kFull, z_acc, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    z_near += __shfl_xor_sync(kFull, z_near, o);
+    z_far += __shfl_xor_sync(kFull, z_far, o);
+  }
   if (lane < G) {
 #pragma unroll
     for (int j = 0; j < V; ++j) s_acc[warp][(j / VEC * G + gl) * VEC + j % VEC] = acc[j];
   }
-  if (lane == 0) s_z[warp] = z_acc;
+  if (lane == 0) {
+    s_z[0][warp] = z_near;
+    s_z[1][warp] = z_far;
+  }
   __syncthreads();
   const int rf = row_floats(N);
   float* my_row = a.part + static_cast<int64_t>(blockIdx.x) * rf;
@@ -302,8 +318,8 @@ __global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(co
     float s = 0.f;
     if (e < N)
       for (int w = 0; w < kBalWarps; ++w) s += s_acc[w][e];
-    else if (e == rf - 4)
-      for (int w = 0; w < kBalWarps; ++w) s += s_z[w];
+    else if (e == rf - 4 || e == rf - 3)
+      for (int w = 0; w < kBalWarps; ++w) s += s_z[e - (rf - 4)][w];
     my_row[e] = s;
   }
   __threadfence();
@@ -333,7 +349,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(co
   }
   s_red[threadIdx.x] = s4;
   __syncthreads();
-  float term = 0.f, z_sum = 0.f;
+  float term = 0.f;
   if (threadIdx.x < quads) {
     for (int i = 1; i < ranges; ++i) {
       const float4 v = s_red[i * quads + q];
@@ -343,7 +359,9 @@ __global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(co
       s4.w += v.w;
     }
     if (q == quads - 1) {
-      z_sum = s4.x;
+      // in fp64: the far sum counts 2^160 times, and z_coef may be 0
+      const double z = static_cast<double>(a.z_coef) * inv_n * (s4.x + s4.y * 0x1p160);
+      s_z[0][0] = static_cast<float>(z);
     } else {
       const float P[4] = {s4.x * inv_n, s4.y * inv_n, s4.z * inv_n, s4.w * inv_n};
 #pragma unroll
@@ -357,23 +375,14 @@ __global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(co
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    term += __shfl_xor_sync(kFull, term, o);
-    z_sum += __shfl_xor_sync(kFull, z_sum, o);
-  }
-  if (lane == 0) {
-    s_z[warp] = z_sum;
-    s_acc[warp][0] = term;
-  }
+  for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(kFull, term, o);
+  if (lane == 0) s_acc[warp][0] = term;
   __syncthreads();
   if (threadIdx.x == 0) {
-    float t = 0.f, z = 0.f;
-    for (int w = 0; w < kBalWarps; ++w) {
-      t += s_acc[w][0];
-      z += s_z[w];
-    }
+    float t = 0.f;
+    for (int w = 0; w < kBalWarps; ++w) t += s_acc[w][0];
     const float balance = a.alpha * static_cast<float>(N) * t;
-    const float zl = a.z_coef * z * inv_n;
+    const float zl = s_z[0][0];
     a.loss[0] = balance + zl;
     a.loss[1] = balance;
     a.loss[2] = zl;

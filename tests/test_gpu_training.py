@@ -726,3 +726,21 @@ def test_training_step_replayed_on_a_side_stream_equals_calls(shape):
         for k in a:
             assert torch.equal(a[k].float(), c[k].float()), k
     assert torch.equal(b1["loss"], b2["loss"]) and int(b2["step"]) == 2
+
+
+# ---------------------------------------------------------------- balance loss, far logits
+@pytest.mark.parametrize("z", [0.0, 1e-3, 1.0])
+@pytest.mark.parametrize("T,N,k", [(3, 256, 8), (200, 8, 2), (5000, 50, 2), (6001, 100, 3)])
+@pytest.mark.parametrize("value", [torch.finfo(torch.float32).min, -1e20, 1e20, -3e14, 2e14])
+def test_balance_loss_of_far_logits(T, N, k, z, value):
+    """Counted rows whose logsumexp has a square past fp32's range: with the z-loss off they add
+    nothing, with it on they add the mean of the squares wherever that is an fp32 number."""
+    L = randn(T, N, seed=T, std=3.0)
+    idx = L.topk(k, 1).indices.to(torch.int32)
+    L[1] = value
+    L[T - 1] = value / 3
+    out = run_balance(L, idx, None, z=z)
+    assert z > 0 or (float(out["loss"][2]) == 0 and bool(torch.isfinite(out["loss"]).all()))
+    check_balance(L, idx, None, z=z, out=out)
+    plain = run_balance(L, idx, None, z=z, grad=False)
+    assert torch.equal(out["loss"], plain["loss"])
