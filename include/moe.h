@@ -437,7 +437,8 @@ typedef struct {
   uint32_t seed;                /* of the stochastic roundings */
   const int32_t* step_dev;      /* device int32 or NULL: t, in place of step, read when the kernel
                                    runs (for captured graphs); below 1 the step is left out */
-  const float* lr_dev;          /* device fp32 or NULL: in place of lr */
+  const float* lr_dev;          /* device fp32 or NULL: in place of lr. Not finite: the step is
+                                   left out (such an lr is refused) */
   const float* grad_scale;      /* device fp32 or NULL (1): multiplies every gradient. Not finite:
                                    the step is left out, nothing is written */
 } moe_adamw_config;

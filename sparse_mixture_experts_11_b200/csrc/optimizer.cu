@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kOptThreads, KIND == kMoments8 ? 4 : 3)
   if (sc.step_dev != nullptr || sc.lr_dev != nullptr) {
     if (sc.step_dev != nullptr) step = *sc.step_dev;
     if (sc.lr_dev != nullptr) rate = *sc.lr_dev;
-    if (step < 1) return;
+    if (step < 1 || !isfinite(rate)) return;
     if (threadIdx.x == 0) {
       s_bc[0] = static_cast<float>(rate / (1.0 - pow(sc.beta1, static_cast<double>(step))));
       s_bc[1] = 1.0f / static_cast<float>(sqrt(1.0 - pow(sc.beta2, static_cast<double>(step))));

@@ -744,3 +744,21 @@ def test_balance_loss_of_far_logits(T, N, k, z, value):
     check_balance(L, idx, None, z=z, out=out)
     plain = run_balance(L, idx, None, z=z, grad=False)
     assert torch.equal(out["loss"], plain["loss"])
+
+
+# ---------------------------------------------------------------- AdamW, a rate that is not finite
+@pytest.mark.parametrize("kind", [("fp32", torch.float32, 32), ("master", torch.bfloat16, 32), ("bf16", torch.float32, 8)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_adamw_leaves_the_step_out_for_a_bad_rate(kind, bad):
+    """A rate read on the device cannot be refused by the call as a number is: the step is left out."""
+    t = make_tensor(1000, kind, seed=2)
+    before = snapshot(t)
+    plan = moe.adamw_plan([descriptor(t, 0.1)])
+    rate = torch.tensor([bad], device="cuda")
+    moe.adamw_step(plan, 3, lr=rate)
+    moe.adamw_step(plan, torch.tensor([3], dtype=torch.int32, device="cuda"), lr=rate)
+    after = snapshot(t)
+    for k in before:
+        assert before[k] is None or np.array_equal(before[k], after[k]), k
+    moe.adamw_step(plan, 3, lr=rate.fill_(1e-3))
+    assert not np.array_equal(before["param"], snapshot(t)["param"])
