@@ -27,7 +27,8 @@
  * moe_adamw_step (the update).
  *
  * Conventions for every call:
- *   - Every pointer is a DEVICE pointer, allocated and owned by the caller, 16-byte aligned.
+ *   - Every pointer is a DEVICE pointer, allocated and owned by the caller, 16-byte aligned (the
+ *     one-element arguments of the training calls: 4-byte aligned).
  *     The library allocates nothing and frees nothing. Its process-wide state is: a cached
  *     driver entry point; per-device kernel attributes and device properties, set or read
  *     once per device; the wait limit of moe_debug_set_wait_timeout_ns; and, for

@@ -52,6 +52,7 @@ inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// One-element arguments may lie anywhere in a buffer of their type.
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -664,7 +665,8 @@ moe_status moe_balance_loss(const moe_dims* dims, const float* logits, const int
   if (!isfinite(alpha) || !isfinite(z_coef)) return MOE_ERR_INVALID;
   if (!aligned16(logits) || !aligned16(topk_idx) || (token_mask && !aligned16(token_mask)) ||
       !aligned16(counts) || !aligned16(prob_mean) || !aligned16(loss) ||
-      (d_logits && !aligned16(d_logits)) || !aligned16(ws))
+      (d_logits && !aligned16(d_logits)) || !aligned16(ws) || !aligned4(n_tokens) ||
+      !aligned4(d_loss))
     return MOE_ERR_UNSUPPORTED;
   if (ws_bytes < stage_ws_bytes(dims)) return MOE_ERR_WORKSPACE;
   if ((st = check_device()) != MOE_OK) return st;
@@ -747,7 +749,7 @@ moe_status moe_grad_norm(const moe_grad_tensor* tensors, int32_t n, float max_no
     if (t.dtype != MOE_DTYPE_F32 && t.dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID;
     if (!aligned16(t.grad)) return MOE_ERR_UNSUPPORTED;
   }
-  if (!aligned16(ws)) return MOE_ERR_UNSUPPORTED;
+  if (!aligned16(ws) || !aligned4(norm) || !aligned4(scale)) return MOE_ERR_UNSUPPORTED;
   size_t need = 0;
   moe_grad_norm_workspace_bytes(&need);
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
@@ -764,6 +766,8 @@ moe_status moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n,
       !(static_cast<float>(c.eps) > 0.f) || !isfinite(static_cast<float>(c.eps)))
     return MOE_ERR_INVALID;
   if (c.step_dev == nullptr && c.step < 1) return MOE_ERR_INVALID;
+  if (!aligned4(c.step_dev) || !aligned4(c.lr_dev) || !aligned4(c.grad_scale))
+    return MOE_ERR_UNSUPPORTED;
   bool any = false;
   for (int32_t i = 0; i < n; ++i) {
     const moe_adamw_tensor& t = tensors[i];

@@ -240,3 +240,13 @@ def test_binding_names_the_argument_at_fault(monkeypatch):
                  lambda: moe._arg(None, 0, "a", torch.float32, (4,)), lambda: moe._arg(z(4, 4).t(), -1, "a", torch.float32, (4, 4))):
         with pytest.raises(ValueError, match="^a "):
             call()
+
+
+@pytest.mark.parametrize("call", [
+    lambda: _balance(_dims(), n=P(18)), lambda: _balance(_dims(), d_loss=P(17)),
+    lambda: _norm([moe.GradTensor(16, 5, 0)], norm=P(18)), lambda: _norm([moe.GradTensor(16, 5, 0)], scale=P(33)),
+    lambda: _adam(config=dict(step_dev=18)), lambda: _adam(config=dict(lr_dev=17)),
+    lambda: _adam(config=dict(grad_scale=19))])
+def test_misaligned_scalars_are_refused(call):
+    """One-element arguments need their type's alignment: an access to any other address would fault."""
+    assert call() == moe.ERR_UNSUPPORTED
