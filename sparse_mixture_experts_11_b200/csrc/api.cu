@@ -683,6 +683,7 @@ moe_status moe_balance_loss(const moe_dims* dims, const float* logits, const int
   a.loss = loss;
   a.d_logits = d_logits;
   a.scratch = shared_region_of(dims, ws);
+  a.scratch_bytes = shared_region_bytes(dims);
   a.counter = reinterpret_cast<int*>(static_cast<char*>(ws) + moe::kBalanceCounterOffset);
   a.T = dims->T;
   a.N = dims->n_experts;

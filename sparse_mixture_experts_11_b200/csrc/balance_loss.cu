@@ -68,8 +68,8 @@ TokenShape token_shape(int N) {
        : N <= 64 ? TokenShape{32, 2, 1} : N <= 128 ? TokenShape{32, 4, 1} : TokenShape{32, 8, 1};
 }
 
-// CTAs of pass 2: one an SM, fewer when the tokens do not fill them.
-int balance_ctas(int64_t T, int N, int most) {
+// CTAs of pass 2: one an SM, fewer when the tokens do not fill them or the workspace has fewer rows.
+int balance_ctas(int64_t T, int N, int64_t most) {
   const int per_cta = kBalWarps * (32 / token_shape(N).g);
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((T + per_cta - 1) / per_cta, most)));
 }
@@ -392,12 +392,13 @@ __global__ void __launch_bounds__(kBalThreads, kBalPerSm) balance_loss_kernel(co
 
 }  // namespace
 
+// The counts and one row. The region that the stages share has a row for every SM's CTA but at a few
+// sizes (N > 200, d_model = 64, 4100 to 5300 tokens: 115 rows at least), where there are fewer CTAs
+// (T = 4300, N = 250 11.5 us, with 148 10.4; T = 5000, N = 256 11.2 and 11.5): asking for more would
+// raise what every stage's call needs.
 size_t balance_scratch_bytes(int64_t T, int N) {
   if (T == 0) return 0;
-  const size_t rows = static_cast<size_t>(count_plan(T).rows) * count_ints(N) * sizeof(int32_t);
-  return rows +
-         static_cast<size_t>(balance_ctas(T, N, kBalanceMaxCtas)) * row_floats(N) *
-             sizeof(float);
+  return static_cast<size_t>(count_plan(T).rows) * count_ints(N) * sizeof(int32_t) + row_floats(N) * sizeof(float);
 }
 
 cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
@@ -419,8 +420,8 @@ cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
   p.d_logits = a.d_logits;
   p.count_rows = static_cast<const int32_t*>(a.scratch);
   p.n_count_rows = cp.rows;
-  p.part = reinterpret_cast<float*>(static_cast<char*>(a.scratch) +
-                                    static_cast<size_t>(cp.rows) * count_ints(a.N) * 4);
+  const size_t count_bytes = static_cast<size_t>(cp.rows) * count_ints(a.N) * sizeof(int32_t);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(a.scratch) + count_bytes);
   p.counter = a.counter;
   p.T = a.T;
   p.N = a.N;
@@ -440,7 +441,8 @@ cudaError_t launch_balance_loss(const BalanceArgs& a, cudaStream_t s) {
     kern = ts.g == 8 ? balance_loss_kernel<8, 1, 1> : ts.g == 16 ? balance_loss_kernel<16, 1, 1>
          : ts.c == 1 ? balance_loss_kernel<32, 1, 1> : ts.c == 2 ? balance_loss_kernel<32, 2, 1>
          : ts.c == 4 ? balance_loss_kernel<32, 4, 1> : balance_loss_kernel<32, 8, 1>;
-  const int grid = balance_ctas(a.T, a.N, std::min(di.sm_count * kBalPerSm, kBalanceMaxCtas));
+  const int64_t rows = (a.scratch_bytes - count_bytes) / (row_floats(a.N) * sizeof(float));
+  const int grid = balance_ctas(a.T, a.N, std::min<int64_t>(di.sm_count * kBalPerSm, rows));
   return launch_pdl(kern, dim3(grid), dim3(kBalThreads), 0, s, p);
 }
 

@@ -301,10 +301,10 @@ struct BackwardArgs {
 size_t backward_router_chunk(int T);
 cudaError_t launch_backward(const BackwardArgs& a, cudaStream_t s);
 
-// Balance loss and z-loss with their gradient (balance_loss.cu). scratch:
-// balance_scratch_bytes(); counter: an int of the workspace's status region, zero between calls.
+// Balance loss and z-loss with their gradient (balance_loss.cu). scratch: balance_scratch_bytes() at
+// least; the grid has no more CTAs than it has rows for. counter: an int of the workspace's status
+// region, zero between calls.
 constexpr size_t kBalanceCounterOffset = 132;
-constexpr int kBalanceMaxCtas = 256;  // CTAs (rows of partial sums) at most
 struct BalanceArgs {
   const float* logits;
   const int32_t* topk_idx;
@@ -317,6 +317,7 @@ struct BalanceArgs {
   float* loss;
   float* d_logits;  // null: no gradient
   void* scratch;
+  size_t scratch_bytes;
   int* counter;
   int T, N, k;
 };

@@ -762,3 +762,22 @@ def test_adamw_leaves_the_step_out_for_a_bad_rate(kind, bad):
         assert before[k] is None or np.array_equal(before[k], after[k]), k
     moe.adamw_step(plan, 3, lr=rate.fill_(1e-3))
     assert not np.array_equal(before["param"], snapshot(t)["param"])
+
+
+@pytest.mark.parametrize("T,d,N", [(5000, 64, 256), (4700, 64, 210), (4097, 64, 255)])
+def test_balance_loss_where_the_workspace_holds_fewer_rows(T, d, N):
+    """Sizes at which the region that the stages share has a row for fewer CTAs than there are SMs:
+    nothing behind the workspace is written, and the result is as good."""
+    dims = moe.make_dims(T, d, N, 2, 64, capacity=T * 2 // N)
+    n = moe.workspace_bytes(dims)
+    buf = torch.zeros(n + 4096, dtype=torch.uint8, device="cuda")
+    buf[n:] = 77
+    L = randn(T, N, seed=N, std=3.0)
+    idx = L.topk(2, 1).indices.to(torch.int32)
+    out = dict(counts=torch.empty(N, dtype=torch.int32, device="cuda"), n=torch.empty(1, dtype=torch.int32, device="cuda"),
+               pm=torch.empty(N, device="cuda"), loss=torch.empty(3, device="cuda"), d=torch.empty(T, N, device="cuda"))
+    for _ in range(2):  # the counter is left as it was found
+        moe.balance_loss(dims, L, idx, None, out["counts"], out["n"], out["pm"], out["loss"], out["d"], buf[:n], z_coef=1e-3)
+        torch.cuda.synchronize()
+        check_balance(L, idx, None, out=out)
+    assert bool((buf[n:] == 77).all())

@@ -250,3 +250,15 @@ def test_binding_names_the_argument_at_fault(monkeypatch):
 def test_misaligned_scalars_are_refused(call):
     """One-element arguments need their type's alignment: an access to any other address would fault."""
     assert call() == moe.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("T,d,N,k,F,stage,forward", [
+    (4096, 128, 256, 8, 64, 240128, 34452224), (5000, 64, 256, 2, 64, 164352, 10599168),
+    (6000, 128, 93, 1, 64, 103936, 7790080), (8192, 128, 256, 8, 64, 282112, 68704000),
+    (5000, 64, 210, 8, 64, 135680, 25566464)])
+def test_balance_loss_leaves_workspace_sizes_alone(T, d, N, k, F, stage, forward):
+    """The sizes of the layer's calls from before there was a balance loss: a workspace of that size
+    is still enough for every one of them, and for the balance loss."""
+    dims = moe.Dims(T=T, d_model=d, n_experts=N, top_k=k, d_ff=F, act=0, capacity=max(1, T * k // N))
+    assert moe.workspace_bytes(dims) == stage and moe.forward_workspace_bytes(dims) == forward
+    assert _balance(dims, nb=stage) != moe.ERR_WORKSPACE and _balance(dims, nb=stage - 1) == moe.ERR_WORKSPACE
