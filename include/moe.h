@@ -368,8 +368,9 @@ moe_status moe_balance_loss(const moe_dims* dims, const float* logits, const int
  *                and must not overlap the inputs
  *   accumulate   0: the outputs are written; 1: added to, as after moe_backward, whose outputs
  *                of the same names have the same shapes
- *   ws, ws_bytes workspace (moe_router_backward_workspace_bytes), no zeroing needed but for its
- *                status word (first 256 bytes; read with moe_read_device_error)
+ *   ws, ws_bytes workspace (moe_router_backward_workspace_bytes: enough for any batch of up to T
+ *                tokens), no zeroing needed but for its status word (first 256 bytes; read with
+ *                moe_read_device_error)
  * Only T, d_model and n_experts of dims matter. Precision: fp32 products and sums. Large batches
  * run on tensor cores, where an fp32 operand is a sum of 16-bit terms (22 bits of it or more) and
  * sums are fp32: within 1e-6 of the exact result in norm. Deterministic for a given device. */

@@ -696,7 +696,7 @@ moe_status moe_router_backward_workspace_bytes(const moe_dims* dims, size_t* byt
   if (st != MOE_OK) return st;
   if (bytes == nullptr) return MOE_ERR_INVALID;
   *bytes = moe::kStatusBytes +
-           round_up(moe::router_backward_scratch_bytes(dims->T, dims->n_experts, dims->d_model), 256);
+           round_up(moe::router_backward_scratch_bytes_up_to(dims->T, dims->n_experts, dims->d_model), 256);
   return MOE_OK;
 }
 
@@ -713,9 +713,8 @@ moe_status moe_router_backward(const moe_dims* dims, const uint16_t* x, const fl
       (d_w_router && !aligned16(d_w_router)) || (d_logit_bias && !aligned16(d_logit_bias)) ||
       !aligned16(ws))
     return MOE_ERR_UNSUPPORTED;
-  size_t need = 0;
-  moe_router_backward_workspace_bytes(dims, &need);
-  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < moe::kStatusBytes + moe::router_backward_scratch_bytes(dims->T, dims->n_experts, dims->d_model))
+    return MOE_ERR_WORKSPACE;
   if ((st = check_device()) != MOE_OK) return st;
   moe::RouterBackwardArgs a{};
   a.x = x;

@@ -340,6 +340,8 @@ struct RouterBackwardArgs {
   uint64_t timeout_ns;
 };
 size_t router_backward_scratch_bytes(int64_t T, int N, int d);
+// Enough for every batch of up to T tokens; does not fall as T grows.
+size_t router_backward_scratch_bytes_up_to(int64_t T, int N, int d);
 cudaError_t launch_router_backward(const RouterBackwardArgs& a, cudaStream_t s);
 
 // Gradient norm and AdamW (optimizer.cu). ws: kStatusBytes, then a double for every CTA; the

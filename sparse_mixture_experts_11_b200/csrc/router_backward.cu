@@ -26,6 +26,7 @@ constexpr int kXTokens = 16, kXCols = 256, kXExperts = 64;
 
 struct Plan {
   int w_cols, w_experts, chunks;  // grid of the W CTAs
+  int64_t most_chunks;            // ranges asked for; never fewer for a larger T
   int64_t chunk;                  // tokens of a range
   int x_cols;
   int64_t x_tokens;               // grid of the x CTAs
@@ -37,8 +38,8 @@ Plan make_plan(int64_t T, int N, int d) {
   p.w_experts = (N + kWExperts - 1) / kWExperts;
   const int64_t tiles = static_cast<int64_t>(p.w_cols) * p.w_experts;
   const int64_t most = (T + 2 * kWTokens - 1) / (2 * kWTokens);  // ranges of at least 64 tokens
-  const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>({most, 2 * 148 / tiles, 64}));
-  p.chunk = (T + chunks - 1) / chunks;
+  p.most_chunks = std::max<int64_t>(1, std::min<int64_t>({most, 2 * 148 / tiles, 64}));
+  p.chunk = (T + p.most_chunks - 1) / p.most_chunks;
   p.chunks = T > 0 ? static_cast<int>((T + p.chunk - 1) / p.chunk) : 0;
   p.x_cols = (d + kXCols - 1) / kXCols;
   p.x_tokens = (T + kXTokens - 1) / kXTokens;
@@ -340,6 +341,7 @@ __host__ __device__ constexpr int w_stages(int group) {
   return (kTcMaxSmem - 1024) / w_stage_bytes(group) < 8 ? (kTcMaxSmem - 1024) / w_stage_bytes(group) : 8;
 }
 
+constexpr int64_t kSplitCtas = 592;  // of split_dl_kernel at most: four an SM
 // Lanes a token takes in split_dl_kernel and pairs of values a lane holds: 2 g p >= N.
 struct SplitShape {
   int g, p;
@@ -349,29 +351,53 @@ SplitShape split_shape(int N) {
        : N <= 64 ? SplitShape{32, 1} : N <= 128 ? SplitShape{32, 2} : SplitShape{32, 4};
 }
 
-TcPlan make_tc_plan(int64_t T, int N, int d) {
+// Waves of 148 CTAs that c token ranges of each tile take, and the cost of a wave besides its tokens:
+// starting and ending a CTA costs about what 128 tokens do.
+int64_t waves(int64_t tiles, int64_t c) { return (tiles * c + 147) / 148; }
+constexpr int64_t kWaveTokens = 128;
+constexpr int64_t kMaxRanges = 32, kMinRange = 256;  // ranges at most, tokens of one at least
+
+// A bound of the number of token ranges for any batch of up to T tokens, which does not fall as T
+// grows. c ranges are chosen over q < c only if waves(c) (t / c + 128) < waves(q) (t / q + 32 + 128),
+// 32 covering the rounding of q's ranges. Both sides are linear in t, so a t in [256 c, T] with that
+// means that one of the ends has it.
+int64_t most_ranges(int64_t T, int64_t tiles) {
+  int64_t most = 1;
+  for (int64_t c = 2; c <= kMaxRanges && T / c >= kMinRange; ++c) {
+    auto over = [&](int64_t q, int64_t t) {
+      return waves(tiles, c) * q * (t + kWaveTokens * c) < waves(tiles, q) * c * (t + (kKb + kWaveTokens) * q);
+    };
+    bool ever = true;
+    for (int64_t q = 1; q < c; ++q) ever = ever && (over(q, kMinRange * c) || over(q, T));
+    if (ever) most = c;
+  }
+  return most;
+}
+
+// for_any: the sizes are enough for every batch of up to T tokens on this path, not this one's own.
+TcPlan make_tc_plan(int64_t T, int N, int d, bool for_any = false) {
   TcPlan p{};
   p.np = (N + 7) / 8 * 8;
   p.group = N <= 32 ? 32 : N <= 64 ? 64 : 128;
   p.planes = p.group == 32 ? 3 : p.group == 64 ? 2 : 1;
   p.n_tiles = (N + p.group - 1) / p.group;
   p.c_tiles = (d + kWTile - 1) / kWTile;
-  // Token ranges: the fewest tokens a CTA in all (whole waves of 148 CTAs), where starting and
-  // ending a CTA costs about what 128 tokens do
+  // Token ranges: the fewest tokens a CTA in all, by whole waves
   const int64_t tiles = static_cast<int64_t>(p.n_tiles) * p.c_tiles;
   int64_t best = 0;
-  for (int64_t c = 1; c <= 32 && (c == 1 || T / c >= 256); ++c) {
+  for (int64_t c = 1; c <= kMaxRanges && (c == 1 || T / c >= kMinRange); ++c) {
     const int64_t len = ((T + c - 1) / c + kKb - 1) / kKb * kKb;
-    const int64_t cost = (tiles * c + 147) / 148 * (len + 128);
+    const int64_t cost = waves(tiles, c) * (len + kWaveTokens);
     if (best == 0 || cost < best) {
       best = cost;
       p.chunk = len;
     }
   }
-  p.chunks = static_cast<int>((T + p.chunk - 1) / p.chunk);
+  p.chunks = static_cast<int>(for_any ? most_ranges(T, tiles) : (T + p.chunk - 1) / p.chunk);
   const int64_t round = kThreads / split_shape(N).g;  // tokens that a CTA splits at once
-  p.split_rows = static_cast<int>(((T + 591) / 592 + round - 1) / round * round);
-  p.split_ctas = static_cast<int>((T + p.split_rows - 1) / p.split_rows);
+  p.split_rows = static_cast<int>(((T + kSplitCtas - 1) / kSplitCtas + round - 1) / round * round);
+  p.split_ctas = static_cast<int>(for_any ? std::min<int64_t>((T + round - 1) / round, kSplitCtas)
+                                          : (T + p.split_rows - 1) / p.split_rows);
   auto r256 = [](size_t v) { return (v + 255) / 256 * 256; };
   p.dl16_bytes = r256(static_cast<size_t>(2) * T * p.np * 2);
   p.dl_bytes = r256(static_cast<size_t>(3) * T * p.np * 2);
@@ -933,7 +959,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // 19.5; (1024, 1024, 64) 18.1, 20.1; (16384, 512, 8) 27.6, 27.9; (64, 4096, 256) 26.5, 22.6; (4096, 512, 64)
 // 30.2, 22.8; (4096, 2880, 32) 69, 32; (1024, 4096, 128) 83, 24. Below 64 tokens a row block of the MMA
 // is half empty.
-bool use_tensor_cores(int64_t T, int N, int d) { return T >= 64 && static_cast<double>(T) * N * d >= 67108864.0; }
+constexpr int64_t kTcMinTokens = 64, kTcMinProducts = 1 << 26;
+bool use_tensor_cores(int64_t T, int N, int d) { return T >= kTcMinTokens && static_cast<double>(T) * N * d >= kTcMinProducts; }
 
 template <int GROUP>
 cudaError_t launch_wgrad(const CUtensorMap& mx, const CUtensorMap& mdl, const CUtensorMap& mp,
@@ -1037,6 +1064,14 @@ size_t router_backward_scratch_bytes(int64_t T, int N, int d) {
   if (use_tensor_cores(T, N, d)) return make_tc_plan(T, N, d).total();
   const Plan p = make_plan(T, N, d);
   return p.chunks > 1 ? static_cast<size_t>(p.chunks) * N * (d + 1) * sizeof(float) : 0;
+}
+
+size_t router_backward_scratch_bytes_up_to(int64_t T, int N, int d) {
+  // the longest batch of these that takes the CUDA cores (see use_tensor_cores), then the tensor cores
+  const int64_t longest = std::max<int64_t>(kTcMinTokens, (kTcMinProducts - 1) / (static_cast<int64_t>(N) * d) + 1) - 1;
+  const Plan p = make_plan(std::min(T, longest), N, d);
+  const size_t cores = p.most_chunks > 1 ? static_cast<size_t>(p.most_chunks) * N * (d + 1) * sizeof(float) : 0;
+  return T > longest ? std::max(cores, make_tc_plan(T, N, d, true).total()) : cores;
 }
 
 cudaError_t launch_router_backward(const RouterBackwardArgs& a, cudaStream_t s) {

@@ -781,3 +781,20 @@ def test_balance_loss_where_the_workspace_holds_fewer_rows(T, d, N):
         torch.cuda.synchronize()
         check_balance(L, idx, None, out=out)
     assert bool((buf[n:] == 77).all())
+
+
+def test_router_backward_workspace_of_a_longer_batch():
+    """A workspace made for 1443 tokens serves 1436, which by itself takes more token ranges."""
+    N, d = 256, 7168
+    n = moe.router_backward_workspace_bytes(moe.make_dims(1443, d, N, 1, 64))
+    buf = torch.zeros(n + 4096, dtype=torch.uint8, device="cuda")
+    buf[n:] = 77
+    for T in (1443, 1436, 70, 1):
+        x, w, g = randn(T, d, seed=T).to(torch.bfloat16), randn(N, d, seed=1, std=d ** -0.5), randn(T, N, seed=2)
+        outs = {k: torch.full(s, float("nan"), device="cuda") for k, s in
+                (("d_x", (T, d)), ("d_w_router", (N, d)), ("d_logit_bias", (N,)))}
+        moe.router_backward(moe.make_dims(T, d, N, 1, 64), x, w, g, *outs.values(), buf[:n])
+        torch.cuda.synchronize()
+        assert moe.read_device_error(buf[:n]) == moe.OK
+        check_router(T, d, N, x, w, g, outs, dict.fromkeys(outs, 0.0), tuple(outs))
+    assert bool((buf[n:] == 77).all())

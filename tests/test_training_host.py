@@ -262,3 +262,25 @@ def test_balance_loss_leaves_workspace_sizes_alone(T, d, N, k, F, stage, forward
     dims = moe.Dims(T=T, d_model=d, n_experts=N, top_k=k, d_ff=F, act=0, capacity=max(1, T * k // N))
     assert moe.workspace_bytes(dims) == stage and moe.forward_workspace_bytes(dims) == forward
     assert _balance(dims, nb=stage) != moe.ERR_WORKSPACE and _balance(dims, nb=stage - 1) == moe.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("N,d", [(256, 7168), (256, 5120), (32, 2880), (8, 128), (64, 1024), (5, 64), (130, 448)])
+def test_router_backward_workspace_serves_shorter_batches(N, d):
+    """The size for a batch is enough for every shorter one: what a call needs itself is not monotone
+    in T (fewer, longer token ranges, or the other path). Every length up to 3000, then a spread."""
+    lengths = list(range(1, 3001)) + [3001 + 211 * i + i * i for i in range(200)] + [2 ** i + j for i in range(12, 21) for j in (-1, 0, 1)]
+    last = 0
+    for T in sorted(lengths):
+        dims = _dims(T=T, n_experts=N, top_k=1, d_model=d)
+        size = moe.router_backward_workspace_bytes(dims)
+        assert size >= last, (T, size, last)
+        last = size
+        assert _router(dims, nb=size) != moe.ERR_WORKSPACE
+
+
+def test_router_backward_workspace_is_not_much_more_than_needed():
+    """At the layers' training batches the size stays what the call itself needs: 4 N and 4 d N bytes a
+    token range, 10 bytes a logit, 4 a token and 4 a weight."""
+    for T, N, d, ranges, planes in ((16384, 256, 7168, 5, 1), (16384, 32, 2880, 12, 3)):
+        need = T * (10 * N + 4) + 4 * N * d * (1 + ranges * planes) + 592 * N * 4 + 4096
+        assert moe.router_backward_workspace_bytes(_dims(T=T, n_experts=N, top_k=1, d_model=d)) <= need
