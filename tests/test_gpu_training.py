@@ -798,3 +798,26 @@ def test_router_backward_workspace_of_a_longer_batch():
         assert moe.read_device_error(buf[:n]) == moe.OK
         check_router(T, d, N, x, w, g, outs, dict.fromkeys(outs, 0.0), tuple(outs))
     assert bool((buf[n:] == 77).all())
+
+
+@pytest.mark.parametrize("T,d,N", [(16384, 2880, 8), (16384, 2880, 64), (16384, 1024, 256)])
+@pytest.mark.parametrize("which", ["d_x", "d_w_router"])
+def test_router_backward_wait_limit_runs_out(T, d, N, which):
+    """Batches whose TMA copies and chains take far longer than an attempt to wait: with a limit of 1 ns
+    each of the two kernels gives up, says so and drains; the next call is right."""
+    dims = moe.make_dims(T, d, N, 1, 64)
+    ws = moe.new_router_backward_workspace(dims)
+    x, w, g = randn(T, d, seed=1).to(torch.bfloat16), randn(N, d, seed=2), randn(T, N, seed=3)
+    outs = dict.fromkeys(("d_x", "d_w_router", "d_logit_bias"))
+    outs[which] = torch.zeros((T, d) if which == "d_x" else (N, d), device="cuda")
+    moe.debug_set_wait_timeout_ns(1)
+    try:
+        moe.router_backward(dims, x, w, g, *outs.values(), ws)
+        torch.cuda.synchronize()
+    finally:
+        moe.debug_set_wait_timeout_ns(0)
+    assert moe.read_device_error(ws) == moe.ERR_TIMEOUT
+    moe.router_backward(dims, x, w, g, *outs.values(), ws)
+    torch.cuda.synchronize()
+    assert moe.read_device_error(ws) == moe.OK
+    check_router(T, d, N, x, w, g, outs, dict.fromkeys(outs, 0.0), (which,))
