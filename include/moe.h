@@ -371,9 +371,16 @@ moe_status moe_balance_loss(const moe_dims* dims, const float* logits, const int
  *   ws, ws_bytes workspace (moe_router_backward_workspace_bytes: enough for any batch of up to T
  *                tokens), no zeroing needed but for its status word (first 256 bytes; read with
  *                moe_read_device_error)
- * Only T, d_model and n_experts of dims matter. Precision: fp32 products and sums. Large batches
- * run on tensor cores, where an fp32 operand is a sum of 16-bit terms (22 bits of it or more) and
- * sums are fp32: within 1e-6 of the exact result in norm. Deterministic for a given device. */
+ * Only T, d_model and n_experts of dims matter. Deterministic for a given device.
+ * Precision: fp32 products and sums. Large batches run on tensor cores, where sums are fp32 (some cut
+ * off, not rounded) and an fp32 operand is a sum of 16-bit terms: d_logits has 24 bits in d_w_router;
+ * in d_x an element of w_router has 22 bits down to 2^-16 of the largest of its row and one of
+ * d_logits down to 2^-16 of the largest d_logits[t, n] max_c |w_router[n, c]| of its token, smaller
+ * ones fewer and fewer, none 2^-38 below. An element of an output that adds n terms is within
+ *   (2 n + 32) 2^-24 S, in d_x on tensor cores + 2^-28 sum_n |d_logits[t, n]| max_c |w_router[n, c]|
+ * of the exact one, S being the sum of its terms' magnitudes (and its old value's). So columns of
+ * w_router that are small in every row have a d_x of few correct bits there. Random operands:
+ * within 1e-6 of S in norm; of the result itself only where its terms do not cancel. */
 moe_status moe_router_backward_workspace_bytes(const moe_dims* dims, size_t* bytes);
 moe_status moe_router_backward(const moe_dims* dims, const uint16_t* x, const float* w_router,
                                const float* d_logits, float* d_x, float* d_w_router,

@@ -280,11 +280,14 @@ cudaError_t launch_sum(const float* part_w, const float* part_b, const RouterBac
 // ------------------------------------------------------------------ tensor-core path
 // Both products have fp32 operands, which are written once as sums of 16-bit terms:
 //   dL^T x   x is exactly bf16, so dL is three bf16 terms (24 bits): three products;
-//   dL W_r   both are two fp16 terms (22 bits) after scaling by powers of two, exact: row n of W_r
-//            by 2^(14 - b_n), b_n the exponent of its largest magnitude, and dL[t, n] by
+//   dL W_r   both are two fp16 terms after scaling by powers of two, exact: row n of W_r by
+//            2^(14 - b_n), b_n the exponent of its largest magnitude, and dL[t, n] by
 //            2^(14 + b_n - a_t), a_t that of the largest dL[t, n] 2^(b_n). Three products (the
 //            fourth is below 2^-22); the result of token t is scaled back by 2^(a_t - 28). Three bf16
-//            terms of each would need six products.
+//            terms of each would need six products. Two terms leave at most 2^-22 of a scaled
+//            operand, or 2^-25 where the second is subnormal (operands 2^-16 below the largest): in
+//            all 3 2^-22 of the products' magnitudes and N 2^-37 of the token's largest dL[t, n]
+//            max_c |W_r[n, c]|, which is what a column small in every row gets.
 // The accumulator of the MMA truncates: measured, a chain of additions loses 1.1e-8 of its value a
 // step of 16 products. dx has 3 N / 16 <= 48 steps. dW's chains would be thousands; they are cut
 // after 48 steps and summed in fp32 registers by the epilogue warps, while the other half of

@@ -821,3 +821,41 @@ def test_router_backward_wait_limit_runs_out(T, d, N, which):
     torch.cuda.synchronize()
     assert moe.read_device_error(ws) == moe.OK
     check_router(T, d, N, x, w, g, outs, dict.fromkeys(outs, 0.0), (which,))
+
+
+# ---------------------------------------------------------------- router backward, the stated precision
+@pytest.mark.parametrize("T,d,N", [(300, 576, 40), (16384, 512, 31), (4096, 1024, 64), (2048, 1024, 256), (8192, 2880, 8)])
+@pytest.mark.parametrize("operands", ["wide", "cancelling", "columns"])
+def test_router_backward_stated_precision(T, d, N, operands):
+    """The bound of include/moe.h, element by element, and its figure in norm, on operands that strain
+    them: magnitudes spread over 40 binades; rows of dL that add up to zero against rows of W_r with a
+    large common part; columns of W_r 2^-30 below the others. The largest d_x floor is the derived
+    (N 2^-37 + 2^-38) sum, at N = 256 just over half of the stated 2^-28."""
+    X, W, G = randn(T, d, seed=1).to(torch.bfloat16), randn(N, d, seed=2), randn(T, N, seed=3)
+    if operands == "wide":
+        W = W * torch.exp2(-(torch.arange(d, device="cuda") % 41).float())
+        G = G * torch.exp2(-(torch.arange(N, device="cuda") % 31).float())
+    elif operands == "columns":
+        W[:, ::3] *= 2.0 ** -30
+    else:
+        p = torch.softmax(2 * G, 1)
+        u = randn(T, N, seed=4)
+        G = p * (u - (p * u).sum(1, keepdim=True))
+        W = W + 100 * randn(1, d, seed=5)
+        X = (X.float() + 10).to(torch.bfloat16)
+    dims = moe.make_dims(T, d, N, 1, 64)
+    ws = moe.new_router_backward_workspace(dims)
+    outs = {k: torch.full(s, float("nan"), device="cuda") for k, s in
+            (("d_x", (T, d)), ("d_w_router", (N, d)), ("d_logit_bias", (N,)))}
+    moe.router_backward(dims, X, W, G, *outs.values(), ws)
+    torch.cuda.synchronize()
+    assert moe.read_device_error(ws) == moe.OK
+    x, w, g = H.f64(X), H.f64(W), H.f64(G)
+    want, size = oracle.router_backward(x, w, g), oracle.router_backward(np.abs(x), np.abs(w), np.abs(g))
+    for name, n in (("d_x", N), ("d_w_router", T), ("d_logit_bias", T)):
+        err = np.abs(H.f64(outs[name]) - want[name])
+        bound = (2 * n + 32) * U * size[name]
+        if name == "d_x":
+            bound = bound + 2.0 ** -28 * (np.abs(g) @ np.abs(w).max(1))[:, None]
+        assert (err <= bound + 1e-37).all(), (name, float((err / (bound + 1e-37)).max()))
+        assert np.linalg.norm(err) <= 1e-6 * np.linalg.norm(size[name]), (name, np.linalg.norm(err) / np.linalg.norm(size[name]))
