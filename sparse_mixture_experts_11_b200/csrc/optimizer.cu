@@ -19,8 +19,11 @@
 // what is kept for the next step is rounded. That rounding is stochastic: a moving average
 // moves by less than half a code step in most steps (v by 0.1 % a step at beta2 = 0.999, the
 // codes lie 6 to 12 % apart), so rounding to nearest would hold it where it is, while up with the
-// probability of the part cut off keeps its expectation. A nonzero r keeps a nonzero code, so
-// that no m is divided by eps alone. The random bits are a function of (seed, step, place of the
+// probability of the part cut off keeps the expectation of m and of r. It is r^2 that the next step
+// reads, and that gains the rounding's variance: with a step of r of d (0.05 % of it, mostly) between
+// codes h apart, h |d| a step, decaying by 1 - beta2, so v settles about (h / r) E|g^2 / v - 1| / 2 above
+// its fp32 value, and as much again at most since the scale moves too (5 to 7 % in the mean for normal
+// and for heavy-tailed gradients). A nonzero r keeps a nonzero code, so that no m is divided by eps alone. The random bits are a function of (seed, step, place of the
 // tensor in the list, element), so a step is reproducible.
 // A bf16 parameter without an fp32 master copy is rounded the same way: most updates are below
 // half its spacing.
