@@ -457,10 +457,13 @@ typedef struct {
 } moe_adamw_config;
 
 /* One AdamW step (decoupled weight decay) over n tensors at once:
- *   g' = g grad_scale,  m' = beta1 m + (1 - beta1) g',  v' = beta2 v + (1 - beta2) g'^2,
- *   p' = p (1 - lr wd) - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
- * in fp32, each operation rounded by itself, in this order. The random bits of a rounding depend
- * on seed, t, the tensor's place in the list and the element, so equal calls give equal results.
+ *   g' = g grad_scale,  m' = beta1 m + [1 - beta1] g',  v' = beta2 v + ([1 - beta2] g') g',
+ *   p' = p [1 - lr wd] - ([lr / (1 - beta1^t)] m') / (sqrt(v') (1 / [sqrt(1 - beta2^t)]) + eps)
+ * in fp32, each operation rounded to nearest by itself, in this order; what stands in brackets is
+ * formed in fp64 and rounded once. The random bits of a rounding depend on seed, t, the tensor's
+ * place in the list and the element, so equal calls give equal results. A call with step_dev or
+ * lr_dev forms the powers on the device, where they may differ in the last place from the host's: it
+ * does not equal one with numbers bit by bit, and a few 8-bit codes may then be other ones.
  * `tensors` and `config` are host memory, read during the call; a graph that captures the call
  * keeps the pointers that they held. A launch takes up to 384 tensors, and large lists a launch
  * for each kind of moments. No workspace. */

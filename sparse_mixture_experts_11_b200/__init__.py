@@ -586,7 +586,8 @@ class _Plan:
 
 
 def grad_plan(grads) -> _Plan:
-    """Descriptors of gradients (fp32 or bf16 tensors of any shape) for grad_norm."""
+    """Descriptors of gradients (fp32 or bf16 tensors of any shape) for grad_norm, made once for
+    buffers that are filled again each step."""
     grads = list(grads)
     items = []
     for i, g in enumerate(grads):
@@ -658,7 +659,8 @@ def adamw_tensor(param, grad, m, v, *, master=None, m_scale=None, v_scale=None,
 
 def adamw_plan(tensors) -> _Plan:
     """Descriptors of many tensors (from adamw_tensor) for adamw_step, made once and used for
-    every step: the plan keeps the tensors alive and their addresses."""
+    every step: the plan keeps the tensors alive and their addresses. Gradients must be in the same
+    buffers every step (as backward_into fills them); tensors elsewhere need another plan."""
     tensors = list(tensors)
     return _Plan(AdamWTensor, [d for d, _ in tensors], [r for _, r in tensors])
 
@@ -667,7 +669,8 @@ def adamw_step(plan: _Plan, step, *, lr=1e-3, betas=(0.9, 0.999), eps: float = 1
                grad_scale=None, stream=None) -> None:
     """One AdamW step over the plan's tensors. step: the number of this step, from 1, or an int32
     tensor [1] read when the kernel runs; lr: a number or an fp32 tensor [1] read likewise;
-    grad_scale: fp32 tensor [1] (from grad_norm) or None."""
+    grad_scale: fp32 tensor [1] (from grad_norm) or None. A rate or scale on the device that is not
+    finite, or a step below 1 there, leaves the step out."""
     here, f32 = _device(), torch.float32
     plan.check(AdamWTensor, here, "adamw_plan")
     step_t = step if isinstance(step, torch.Tensor) else None

@@ -8,9 +8,10 @@
 //
 // AdamW (decoupled weight decay), element by element:
 //   g' = g * grad_scale
-//   m' = beta1 m + (1 - beta1) g',   v' = beta2 v + (1 - beta2) g'^2
-//   p' = p (1 - lr wd) - lr / (1 - beta1^t) * m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
-// All of it is fp32. What bounds it is HBM: it reads and writes every state once and shares
+//   m' = beta1 m + (1 - beta1) g',   v' = beta2 v + ((1 - beta2) g') g'
+//   p' = p (1 - lr wd) - (lr / (1 - beta1^t) m') / (sqrt(v') c + eps),   c = 1 / sqrt(1 - beta2^t)
+// All of it is fp32; what does not depend on the element is formed once, in fp64, and rounded (c: the
+// root is rounded, then its reciprocal). What bounds it is HBM: it reads and writes every state once and shares
 // nothing between elements.
 //
 // Moments in 8 bits: m and r = sqrt(v) are held as E4M3 codes with one fp32 scale per 128
@@ -31,7 +32,8 @@
 // Where a value lies next to a border of the codes, its last bit decides between codes 6 to 12 %
 // apart, and a block's next scale can hang on one code. So every fp32 operation is rounded by
 // itself, in the order of the formulas (no fused multiply-add; square root, quotient and
-// reciprocal to nearest): any fp32 implementation of these lines has the same results, bit by bit.
+// reciprocal to nearest), a block's scale being top (1 / 448) and its values times (1 / top) 448: any
+// fp32 implementation of these lines has the same results, bit by bit.
 // 537M elements with masters took 2365 us so and 2305 with approximate roots and quotients.
 #include <math.h>
 
