@@ -319,8 +319,8 @@ __device__ __forceinline__ uint64_t desc_k64(uint32_t addr) {
 }
 
 // True on one lane, always the same one. The MMA warp runs its loops as a whole and elects a lane for
-// each instruction: the operands stay warp-uniform, where a branch on the lane around the loops
-// makes every one of them move to a uniform register first (about 100 cycles an MMA).
+// each instruction: loops, waits and operands stay uniform over the warp. With a branch on the lane
+// around the loops dW took 36 us at T = 16384, N = 32, d = 2880, and 29 so.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
