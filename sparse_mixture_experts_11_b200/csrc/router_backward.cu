@@ -960,8 +960,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // Tensor cores where the products are worth the five launches, from T N d = 2^26 on. Device time
 // of the two paths, CUDA cores first, us, at (T, d, N): (256, 1024, 64) 11.3, 18.3; (512, 2880, 32) 15.9,
 // 19.5; (1024, 1024, 64) 18.1, 20.1; (16384, 512, 8) 27.6, 27.9; (64, 4096, 256) 26.5, 22.6; (4096, 512, 64)
-// 30.2, 22.8; (4096, 2880, 32) 69, 32; (1024, 4096, 128) 83, 24. Below 64 tokens a row block of the MMA
-// is half empty.
+// 30.2, 22.8; (4096, 2880, 32) 69, 32; (1024, 4096, 128) 83, 24. At the threshold itself either may be
+// ahead, by 2 us at most of those measured. Below 64 tokens a row block of the MMA is half empty.
 constexpr int64_t kTcMinTokens = 64, kTcMinProducts = 1 << 26;
 bool use_tensor_cores(int64_t T, int N, int d) { return T >= kTcMinTokens && static_cast<double>(T) * N * d >= kTcMinProducts; }
 
