@@ -11,8 +11,8 @@
 //   m' = beta1 m + (1 - beta1) g',   v' = beta2 v + ((1 - beta2) g') g'
 //   p' = p (1 - lr wd) - (lr / (1 - beta1^t) m') / (sqrt(v') c + eps),   c = 1 / sqrt(1 - beta2^t)
 // All of it is fp32; what does not depend on the element is formed once, in fp64, and rounded (c: the
-// root is rounded, then its reciprocal). What bounds it is HBM: it reads and writes every state once and shares
-// nothing between elements.
+// root is rounded, then its reciprocal). What bounds it is HBM: it reads and writes every state once
+// and shares nothing between elements.
 //
 // Moments in 8 bits: m and r = sqrt(v) are held as E4M3 codes with one fp32 scale per 128
 // elements, amax / 448. sqrt(v) and not v, because E4M3's 18 binades then cover 36 binades of v,
@@ -24,8 +24,9 @@
 // reads, and that gains the rounding's variance: with a step of r of d (0.05 % of it, mostly) between
 // codes h apart, h |d| a step, decaying by 1 - beta2, so v settles about (h / r) E|g^2 / v - 1| / 2 above
 // its fp32 value, and as much again at most since the scale moves too (5 to 7 % in the mean for normal
-// and for heavy-tailed gradients). A nonzero r keeps a nonzero code, so that no m is divided by eps alone. The random bits are a function of (seed, step, place of the
-// tensor in the list, element), so a step is reproducible.
+// and for heavy-tailed gradients). A nonzero r keeps a nonzero code, so that no m is divided by eps
+// alone. The random bits are a function of (seed, step, place of the tensor in the list, element), so a
+// step is reproducible.
 // A bf16 parameter without an fp32 master copy is rounded the same way: most updates are below
 // half its spacing.
 //
